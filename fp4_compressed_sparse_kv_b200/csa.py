@@ -59,7 +59,8 @@ EXPORTS = ["csa_workspace_bytes", "csa_workspace_init", "csa_kv_pack_fp4", "csa_
            "csa_indexer_reindex", "csa_indexer_block_scores", "csa_topk_blocks", "csa_index_reuse", "csa_sparse_decode_attn", "csa_decode_layer",
            "csa_check_device_error", "csa_status_string", "csa_indexer_full_noalloc",
            "csa_indexer_screen_bounds", "csa_kv_norm_rope_pack_fp4", "csa_candidates_concat",
-           "csa_shard_blocks", "csa_attn_merge", "csa_kv_record_bytes", "csa_kv_export", "csa_kv_import"]
+           "csa_shard_blocks", "csa_attn_merge", "csa_kv_record_bytes", "csa_kv_export", "csa_kv_import",
+           "csa_kv_append_fp4", "csa_kv_unpack_fp4", "csa_dense_attn_workspace_bytes", "csa_dense_attn"]
 
 _lib = None
 
@@ -120,6 +121,16 @@ def lib():
     L.csa_kv_export.argtypes = [ctypes.POINTER(KVLayerC), P, i32, P, P, sz, P]
     L.csa_kv_import.restype = st
     L.csa_kv_import.argtypes = [ctypes.POINTER(KVLayerC), P, i32, P, P, sz, P]
+    L.csa_kv_append_fp4.restype = st
+    L.csa_kv_append_fp4.argtypes = [ctypes.POINTER(KVLayerC), ctypes.POINTER(BatchC), P, i32, P, P, P, P, i32, P,
+                                    sz, P]
+    L.csa_kv_unpack_fp4.restype = st
+    L.csa_kv_unpack_fp4.argtypes = [ctypes.POINTER(KVLayerC), ctypes.POINTER(BatchC), P, i32, P, P, sz, P]
+    L.csa_dense_attn_workspace_bytes.restype = sz
+    L.csa_dense_attn_workspace_bytes.argtypes = []
+    L.csa_dense_attn.restype = st
+    L.csa_dense_attn.argtypes = [ctypes.POINTER(KVLayerC), ctypes.POINTER(BatchC), P, i32, P, i32, ctypes.c_float,
+                                 ctypes.c_float, P, P, P, P, P, sz, P]
     L.csa_check_device_error.restype = st
     L.csa_check_device_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_int64)]
     L.csa_status_string.restype = ctypes.c_char_p
@@ -400,6 +411,66 @@ def kv_import(layer, block_table, n, src, ws, stream=None):
     lc, bt, s = _record_args(layer, block_table, n, src, "src")
     _check(lib().csa_kv_import(ctypes.byref(lc), bt, int(n), s, _ptr(ws, "ws"), ws.numel(), _stream(stream)),
            "csa_kv_import")
+
+
+def _run_rows(batch, cu_rows, rows, **arrays):
+    """Rows of a ragged run: checks cu_rows and that every array has the dtype and shape given for it."""
+    if cu_rows.dtype != torch.int32 or cu_rows.numel() != batch.B + 1:
+        raise ValueError("cu_rows must be int32 with batch.B + 1 entries")
+    for name, (t, dtype, shape) in arrays.items():
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
+            raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
+    return int(rows)
+
+
+def kv_append_fp4(layer, batch, cu_rows, latent, idx_key, ws, norm_weight=None, rope_table=None, stream=None):
+    """Write a ragged run into the caches by position: rows cu_rows[b] .. cu_rows[b+1] - 1 of latent
+    (bf16 [rows, 512]) and idx_key (bf16 [rows, 128]) are the last positions of sequence b (batch.seq_len
+    counts them).  norm_weight float32 [512] and rope_table float32 [positions, 32, 2] of (cos, sin) apply
+    RMSNorm and the rotation of each row's position first; the last 128 positions also go to the window."""
+    rows = _run_rows(batch, cu_rows, latent.shape[0], latent=(latent, torch.bfloat16, (latent.shape[0], LATENT)),
+                     idx_key=(idx_key, torch.bfloat16, (latent.shape[0], IDX_DIM)),
+                     norm_weight=(norm_weight, torch.float32, (LATENT,)))
+    if rope_table is not None and (rope_table.dtype != torch.float32 or tuple(rope_table.shape[1:]) != (32, 2)):
+        raise ValueError("rope_table must be float32 of shape [positions, 32, 2]")
+    lc, bc = layer.c(), batch.c()
+    _check(lib().csa_kv_append_fp4(ctypes.byref(lc), ctypes.byref(bc), _ptr(cu_rows, "cu_rows"), rows,
+                                   _ptr(latent, "latent"), _ptr(idx_key, "idx_key"), _ptr(norm_weight, "norm_weight"),
+                                   _ptr(rope_table, "rope_table"), 0 if rope_table is None else rope_table.shape[0],
+                                   _ptr(ws, "ws"), ws.numel(), _stream(stream)), "csa_kv_append_fp4")
+
+
+def kv_unpack_fp4(layer, batch, cu_rows, latent, ws, stream=None):
+    """Read a ragged run's FP4 entries back as values into latent, bf16 [rows, 512] (exact)."""
+    rows = _run_rows(batch, cu_rows, latent.shape[0], latent=(latent, torch.bfloat16, (latent.shape[0], LATENT)))
+    lc, bc = layer.c(), batch.c()
+    _check(lib().csa_kv_unpack_fp4(ctypes.byref(lc), ctypes.byref(bc), _ptr(cu_rows, "cu_rows"), rows,
+                                   _ptr(latent, "latent"), _ptr(ws, "ws"), ws.numel(), _stream(stream)),
+           "csa_kv_unpack_fp4")
+
+
+def dense_attn_workspace(device="cuda", stream=None):
+    """Allocate (with torch) and initialise a workspace for dense_attn; one size serves every call."""
+    ws = torch.empty(lib().csa_dense_attn_workspace_bytes(), dtype=torch.uint8, device=device)
+    workspace_init(ws, stream)
+    return ws
+
+
+def dense_attn(layer, batch, cu_rows, q, out, lse, ws, sm_scale=None, softcap=0.0, slopes=None, spans=None,
+               stream=None):
+    """Attention of a ragged run's queries q (bf16 [rows, H, 512], H <= 128) over every visible position of
+    the FP4 cache: out bf16 [rows, H, 512], lse float32 [rows, H].  Causal, or spans int32 [rows, 2] of the
+    positions lo <= j < hi each row sees; softcap > 0 caps scores by softcap * tanh(s / softcap); slopes
+    float32 [H] subtracts slopes[h] * |p - j|."""
+    R, H = int(q.shape[0]), int(q.shape[1])
+    rows = _run_rows(batch, cu_rows, R, q=(q, torch.bfloat16, (R, H, LATENT)), out=(out, torch.bfloat16, (R, H, LATENT)),
+                     lse=(lse, torch.float32, (R, H)), slopes=(slopes, torch.float32, (H,)),
+                     spans=(spans, torch.int32, (R, 2)))
+    lc, bc = layer.c(), batch.c()
+    _check(lib().csa_dense_attn(ctypes.byref(lc), ctypes.byref(bc), _ptr(cu_rows, "cu_rows"), rows, _ptr(q, "q"), H,
+                                float(default_sm_scale() if sm_scale is None else sm_scale), float(softcap),
+                                _ptr(slopes, "slopes"), _ptr(spans, "spans"), _ptr(out, "out"), _ptr(lse, "lse"),
+                                _ptr(ws, "ws"), ws.numel(), _stream(stream)), "csa_dense_attn")
 
 
 def check_device_error(ws, stream=None):

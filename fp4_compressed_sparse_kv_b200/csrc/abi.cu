@@ -4,6 +4,8 @@
 
 #include "attention_common.cuh"
 #include "common.cuh"
+#include "dense_attn.cuh"
+#include "runs.cuh"
 
 namespace csa {
 
@@ -22,6 +24,10 @@ cudaError_t launch_block_scores_full_or_pool(const uint8_t *keys, int num_pages,
                                              const uint16_t *iq, const float *iw, const int32_t *pool,
                                              const int32_t *pool_count, int pool_cap, float *scores,
                                              int score_stride, void *ws, cudaStream_t st);
+cudaError_t launch_kv_append(const csa_kv_layer &layer, const Runs &r, const uint16_t *latent, const uint16_t *idx_key,
+                             const float *norm_w, const float *rope_table, int rope_positions, void *ws,
+                             cudaStream_t st);
+cudaError_t launch_kv_unpack(const csa_kv_layer &layer, const Runs &r, uint16_t *latent, void *ws, cudaStream_t st);
 bool screen_supported(int num_pages);
 cudaError_t launch_screen_bounds(const uint8_t *keys, int num_pages, const csa_batch &bt, const uint16_t *iq,
                                  const float *iw, uint8_t *qt, void *qm, uint32_t *hist, uint32_t *hist2, float *lo,
@@ -68,6 +74,20 @@ bool batch_ok(const csa_batch *b)
 }
 
 bool heads_ok(int H) { return H == 16 || H == 32 || H == 64 || H == 128; }
+
+// Arguments that every call over a ragged run takes.
+csa_status check_run(const csa_kv_layer *layer, const csa_batch *batch, const int32_t *cu_rows, int32_t rows,
+                     const void *ws, size_t ws_bytes, size_t need)
+{
+    if (!layer_ok(layer, layer && layer->swa) || !batch_ok(batch)) return CSA_ERR_INVALID_ARG;
+    if (rows > CSA_MAX_SEQ_LEN || !cu_rows || !aligned16(cu_rows) || !ws || !aligned16(ws)) return CSA_ERR_INVALID_ARG;
+    return ws_bytes < need ? CSA_ERR_WORKSPACE : CSA_OK;
+}
+
+Runs runs_of(const csa_batch &b, const int32_t *cu_rows, int32_t rows)
+{
+    return Runs{b.B, rows, cu_rows, b.seq_len, b.block_table, b.max_pages, b.max_seq_len, b.swa_row};
+}
 
 WsLayout layout_for(int B, int H, int max_seq_len, int cap)
 {
@@ -343,6 +363,76 @@ csa_status csa_decode_layer(const csa_kv_layer *layer, const csa_batch *batch, c
     if (s != CSA_OK) return s;
     return csa_sparse_decode_attn(layer, batch, p->q, p->H, p->sm_scale, p->blocks, p->count, p->cap, p->out,
                                   p->lse, ws, ws_bytes, stream);
+}
+
+csa_status csa_kv_append_fp4(const csa_kv_layer *layer, const csa_batch *batch, const int32_t *cu_rows, int32_t rows,
+                             const uint16_t *latent, const uint16_t *idx_key, const float *norm_weight,
+                             const float *rope_table, int32_t rope_positions, void *ws, size_t ws_bytes, void *stream)
+{
+    if (rows < 0) return CSA_ERR_INVALID_ARG;
+    if (rows == 0) return CSA_OK;
+    const csa_status s = check_run(layer, batch, cu_rows, rows, ws, ws_bytes, kHeaderBytes);
+    if (s != CSA_OK) return s;
+    if (!latent || !idx_key || !aligned16(latent) || !aligned16(idx_key) || !aligned16(norm_weight) ||
+        !aligned16(rope_table))
+        return CSA_ERR_INVALID_ARG;
+    if (rope_table && rope_positions < 1) return CSA_ERR_INVALID_ARG;
+    return cuda_status(launch_kv_append(*layer, runs_of(*batch, cu_rows, rows), latent, idx_key, norm_weight, rope_table,
+                                        rope_positions, ws, (cudaStream_t)stream));
+}
+
+csa_status csa_kv_unpack_fp4(const csa_kv_layer *layer, const csa_batch *batch, const int32_t *cu_rows, int32_t rows,
+                             uint16_t *latent, void *ws, size_t ws_bytes, void *stream)
+{
+    if (rows < 0) return CSA_ERR_INVALID_ARG;
+    if (rows == 0) return CSA_OK;
+    const csa_status s = check_run(layer, batch, cu_rows, rows, ws, ws_bytes, kHeaderBytes);
+    if (s != CSA_OK) return s;
+    if (!latent || !aligned16(latent)) return CSA_ERR_INVALID_ARG;
+    return cuda_status(launch_kv_unpack(*layer, runs_of(*batch, cu_rows, rows), latent, ws, (cudaStream_t)stream));
+}
+
+size_t csa_dense_attn_workspace_bytes(void) { return dense_ws_layout().total; }
+
+csa_status csa_dense_attn(const csa_kv_layer *layer, const csa_batch *batch, const int32_t *cu_rows, int32_t rows,
+                          const uint16_t *q, int32_t H, float sm_scale, float softcap, const float *slopes,
+                          const int32_t *spans, uint16_t *out, float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    if (rows < 0) return CSA_ERR_INVALID_ARG;
+    if (rows == 0) return CSA_OK;
+    const DenseWs w = dense_ws_layout();
+    const csa_status s = check_run(layer, batch, cu_rows, rows, ws, ws_bytes, w.total);
+    if (s != CSA_OK) return s;
+    if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(slopes) ||
+        !aligned16(spans))
+        return CSA_ERR_INVALID_ARG;
+    if (H < 1 || H > 128) return CSA_ERR_UNSUPPORTED;
+    if (!(sm_scale > 0.f) || sm_scale > 1e30f || !(softcap >= 0.f) || softcap > 1e30f) return CSA_ERR_INVALID_ARG;
+    char *base = (char *)ws;
+    DenseArgs a;
+    a.codes = layer->codes;
+    a.scales = layer->scales;
+    a.num_pages = layer->num_pages;
+    a.B = batch->B;
+    a.seq_len = batch->seq_len;
+    a.block_table = batch->block_table;
+    a.max_pages = batch->max_pages;
+    a.max_seq_len = batch->max_seq_len;
+    a.cu_rows = cu_rows;
+    a.rows = rows;
+    a.q = q;
+    a.H = H;
+    a.sm_scale = sm_scale;
+    a.softcap = softcap;
+    a.slopes = slopes;
+    a.spans = reinterpret_cast<const int2 *>(spans);
+    a.out = out;
+    a.lse = lse;
+    a.share = reinterpret_cast<DenseShare *>(base + w.share);
+    a.part_ml = reinterpret_cast<float2 *>(base + w.part_ml);
+    a.part_o = reinterpret_cast<float *>(base + w.part_o);
+    a.ws = ws;
+    return cuda_status(launch_dense_attn(a, (cudaStream_t)stream));
 }
 
 csa_status csa_check_device_error(void *ws, void *stream, int64_t *detail)

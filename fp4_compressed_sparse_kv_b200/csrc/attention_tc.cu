@@ -40,8 +40,7 @@
 // Softmax rescales lazily: O^T is rescaled in TMEM only when a head's running maximum grows by more
 // than 2^8 (after waiting for the previous tile's PV).
 #include "attention_common.cuh"
-#include "pipeline.cuh"
-#include "tcgen05.cuh"
+#include "attention_tile.cuh"
 
 namespace csa {
 
@@ -68,11 +67,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;                    // O^T: M-tile m in columns 64m .. 64m+63
 constexpr uint32_t kColQ = 256;                  // Q_x: 128 columns in lane half x
 constexpr uint32_t kColS = 384;                  // S_x of tile t: columns 384 + 64(t%2) in lane half x
-constexpr float kLazy = 8.f;      // log2-domain growth of a head maximum tolerated without rescaling
-constexpr float kPOffset = 7.f;   // p = exp2(z - m + 7) <= 2^15 keeps small p out of fp16 subnormals
-constexpr float kNoMax = -1e30f;  // running maximum before any finite score (exp2 of it minus a finite value is 0)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct TcMisc {
     uint64_t q_ready, o_done;
@@ -93,60 +87,8 @@ constexpr size_t kTcSmem = kOffMisc + sizeof(TcMisc) + 1024;
 constexpr uint32_t kIdescQK = umma_idesc_f16(64, kTile, false, false);
 constexpr uint32_t kIdescPV = umma_idesc_f16(128, kTcHeads, true, false);
 
-__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t unit) { return row * 128u + ((unit ^ (row & 7u)) << 4); }
-
-__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
-{
-    __half2 x = *reinterpret_cast<__half2 *>(&a), y = *reinterpret_cast<__half2 *>(&b);
-    __half2 r = __hmul2(x, y);
-    return *reinterpret_cast<uint32_t *>(&r);
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&h);
-}
-
 // Named barriers: 1 = the softmax warps (128 threads); 3 = the producers (512); 4 = every warp (768).
 // Every participant executes each of them the same number of times, also after a failed wait.
-__device__ __forceinline__ bool bar_and(int id, int n, bool v)
-{
-    int r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %3, 0;\nbar.red.and.pred p, %1, %2, q;\nselp.b32 %0, 1, 0, p;\n}"
-                 : "=r"(r)
-                 : "r"(id), "r"(n), "r"((int)v)
-                 : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ bool bar_or(int id, int n, bool v)
-{
-    int r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 q, %3, 0;\nbar.red.or.pred p, %1, %2, q;\nselp.b32 %0, 1, 0, p;\n}"
-                 : "=r"(r)
-                 : "r"(id), "r"(n), "r"((int)v)
-                 : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-
-// 32 lanes x 16 consecutive 32-bit columns (thread i: lane i), waited for in the same statement.
-__device__ __forceinline__ void tc_ld16_sync(uint32_t taddr, float *v)
-{
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 
 // Tile-aligned split of a sequence's units: split s of `splits` gets whole 8-unit tiles, so every
 // tile but the sequence's last is full.
@@ -274,73 +216,6 @@ __device__ __forceinline__ void fill_table(const AttnArgs &a, TcMisc &ms, int32_
 #pragma unroll
         for (int j = 0; j < kAttnUnit; ++j) out[j] = -1;
     }
-}
-
-__device__ __forceinline__ void tc_st16_u(uint32_t taddr, const uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
-// 32 lanes x 8 consecutive 32-bit columns (thread i: lane i), waited for in the same statement; and
-// the matching store.
-__device__ __forceinline__ void tc_ld8_sync(uint32_t taddr, float *v)
-{
-    uint32_t r[8];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void tc_st8(uint32_t taddr, const float *v)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-                 "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-                 : "memory");
-}
-
-// Two loads of 16 lanes x 16 columns with a half-warp split: thread i < 16 gets lane base+i, columns
-// [col, col+16) and thread i >= 16 lane base+i-16, columns [col+32, col+48), from each address; one
-// wait for both in the same statement.
-__device__ __forceinline__ void tc_ld16x32bx2_x16_pair(uint32_t ta, uint32_t tb, float *a, float *b)
-{
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32], 32;\n"
-        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-        "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33], 32;\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(ta), "r"(tb)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        a[i] = __uint_as_float(r[i]);
-        b[i] = __uint_as_float(r[16 + i]);
-    }
-}
-
-// One arrival per warp: every lane's earlier writes (and its proxy or tcgen05 fences) are ordered
-// before lane 0's arrive by the warp barrier.  Barriers that warps arrive on count warps.
-__device__ __forceinline__ void warp_arrive(uint64_t *bar)
-{
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // Q of heads h0..h0+63 into TMEM as the A operand of the QK MMAs, scaled by one power of two 2^k that

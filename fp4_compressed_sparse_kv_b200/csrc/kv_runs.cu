@@ -1,0 +1,160 @@
+// kv_runs.cu -- append a ragged run of tokens to the paged FP4 cache by position, and read one back.
+//
+// rebasdaily article on DeepSeek-V4.1-Flash KV compression, section "同一份笔记，多层一起用" (FP4 main
+// KV, FP8 window) and section "先让长输入少走一半路" (the window holds the most recent tokens); yomxxx.com
+// long-form post, section 五 (addresses computed from the token index).
+//
+// Append: one warp per token, or four consecutive tokens per warp for long calls, as in pack.cu, whose
+// arithmetic (pack_token.cuh) it shares; the token's sequence, page, rotation and window slot are worked
+// out from its row number, so the caller builds no slot or angle arrays and no pass over the latents
+// comes before the pack.  Unpack: the inverse for the FP4 entries, e2m1 * e4m3 in bf16, which is exact
+// (at most 6 significant bits); a lane converts two pieces of 8 channels so that a warp's stores are
+// 512 contiguous bytes.  Both stream their bytes once and are bound by HBM for long calls, by the chain
+// of dependent metadata loads (cu_rows, then the page id, then the entry) for short ones.
+#include "pack_token.cuh"
+#include "pipeline.cuh"
+#include "runs.cuh"
+
+namespace csa {
+
+constexpr int kRunWarps = 8;             // warps per CTA
+constexpr int kRunTokLarge = 4;          // tokens per warp of a long call
+constexpr int kRunLargeFrom = 4096;      // rows from which warps take kRunTokLarge tokens
+
+template <bool kNorm, bool kRope, int kTok>
+__global__ void __launch_bounds__(32 * kRunWarps) kv_append_kernel(csa_kv_layer layer, Runs r,
+                                                                   const uint16_t *__restrict__ latent,
+                                                                   const uint16_t *__restrict__ idx_key,
+                                                                   const float *__restrict__ norm_w,
+                                                                   const float *__restrict__ rope_table,
+                                                                   int rope_positions, void *ws)
+{
+    grid_dep_launch();   // a dependent kernel waits for this grid before it reads the caches
+    const int t0 = (blockIdx.x * kRunWarps + (threadIdx.x >> 5)) * kTok;
+    const int lane = threadIdx.x & 31;
+    if (t0 == 0 && lane == 0 && r.cu_rows[r.B] > r.rows) report(ws, CSA_ERR_DEVICE_DATA, r.B);
+    PackIn in[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+        const int t = t0 + i;
+        if (t < r.rows) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(latent + (size_t)t * kLatent) + 2 * lane;
+            in[i].a = src[0];
+            in[i].b = src[1];
+            in[i].kw = reinterpret_cast<const uint2 *>(idx_key + (size_t)t * kIdxDim)[lane];
+        }
+    }
+    RowPlace p[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+        const int t = t0 + i;
+        p[i].seq = -1;
+        if (t < r.rows) {
+            p[i] = warp_place_row(r, t, layer.num_pages);
+            if (kRope && p[i].pos >= rope_positions) {
+                p[i].bad = true;
+                p[i].seq = -1;
+            }
+            if (p[i].bad && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
+            in[i].s = p[i].slot;
+            in[i].ss = -1;
+            if (p[i].seq >= 0 && layer.swa && p[i].pos >= p[i].len - kWindow) {
+                const int row = r.swa_row[p[i].seq];
+                if (row >= 0 && row < layer.num_rows) in[i].ss = row * kWindow + p[i].pos % kWindow;
+                else if (row != -1 && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+        if (p[i].seq >= 0)
+            pack_token<kNorm, kRope>(layer, in[i], t0 + i, lane, ws, norm_w,
+                                     kRope ? rope_table + (size_t)p[i].pos * kRopeRow : nullptr);
+}
+
+
+template <int kTok>
+__global__ void __launch_bounds__(32 * kRunWarps) kv_unpack_kernel(csa_kv_layer layer, Runs r,
+                                                                   uint16_t *__restrict__ latent, void *ws)
+{
+    grid_dep_launch();
+    const int t0 = (blockIdx.x * kRunWarps + (threadIdx.x >> 5)) * kTok;
+    const int lane = threadIdx.x & 31;
+    if (t0 == 0 && lane == 0 && r.cu_rows[r.B] > r.rows) report(ws, CSA_ERR_DEVICE_DATA, r.B);
+    int64_t slot[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+        slot[i] = -1;
+        if (t0 + i < r.rows) {
+            const RowPlace p = warp_place_row(r, t0 + i, layer.num_pages);
+            if (p.bad && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t0 + i);
+            if (p.seq >= 0) slot[i] = p.slot;
+        }
+    }
+    // lane: channels 256 j + 8 lane .. + 7 for j = 0, 1
+    uint32_t code[kTok][2];
+    uint8_t scale[kTok][2];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (slot[i] >= 0) {
+                code[i][j] = reinterpret_cast<const uint32_t *>(layer.codes + slot[i] * kCodeBytes)[32 * j + lane];
+                scale[i][j] = layer.scales[slot[i] * kScaleBytes + 16 * j + (lane >> 1)];
+            }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (slot[i] >= 0) {
+                uint32_t c[4], o[4];
+                e2m1x8_to_f16x2x4(code[i][j], c);
+                const float s = e4m3_to_f32(scale[i][j]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    __nv_bfloat162 v = __floats2bfloat162_rn(h_lo(c[k]) * s, h_hi(c[k]) * s);
+                    o[k] = *reinterpret_cast<uint32_t *>(&v);
+                }
+                reinterpret_cast<uint4 *>(latent + (size_t)(t0 + i) * kLatent)[32 * j + lane] =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+}
+
+template <bool kNorm, bool kRope>
+static cudaError_t append(const csa_kv_layer &layer, const Runs &r, const uint16_t *latent, const uint16_t *idx_key,
+                          const float *norm_w, const float *rope_table, int rope_positions, void *ws, cudaStream_t st)
+{
+    if (r.rows >= kRunLargeFrom) {
+        const int per = kRunWarps * kRunTokLarge;
+        kv_append_kernel<kNorm, kRope, kRunTokLarge><<<(r.rows + per - 1) / per, 32 * kRunWarps, 0, st>>>(
+            layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws);
+    } else {
+        kv_append_kernel<kNorm, kRope, 1><<<(r.rows + kRunWarps - 1) / kRunWarps, 32 * kRunWarps, 0, st>>>(
+            layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const csa_kv_layer &layer, const Runs &r, const uint16_t *latent, const uint16_t *idx_key,
+                             const float *norm_w, const float *rope_table, int rope_positions, void *ws,
+                             cudaStream_t st)
+{
+    if (norm_w && rope_table)
+        return append<true, true>(layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws, st);
+    if (norm_w) return append<true, false>(layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws, st);
+    if (rope_table) return append<false, true>(layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws, st);
+    return append<false, false>(layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws, st);
+}
+
+cudaError_t launch_kv_unpack(const csa_kv_layer &layer, const Runs &r, uint16_t *latent, void *ws, cudaStream_t st)
+{
+    if (r.rows >= kRunLargeFrom) {
+        const int per = kRunWarps * kRunTokLarge;
+        kv_unpack_kernel<kRunTokLarge><<<(r.rows + per - 1) / per, 32 * kRunWarps, 0, st>>>(layer, r, latent, ws);
+    } else {
+        kv_unpack_kernel<1><<<(r.rows + kRunWarps - 1) / kRunWarps, 32 * kRunWarps, 0, st>>>(layer, r, latent, ws);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace csa

@@ -376,6 +376,64 @@ csa_status csa_kv_export(const csa_kv_layer *layer, const int32_t *block_table, 
 csa_status csa_kv_import(const csa_kv_layer *layer, const int32_t *block_table, int32_t n, const uint8_t *src,
                          void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Ragged runs over the FP4 main cache.  The pages have no counterpart to these entry points; they serve
+ * what surrounds the sparse decode step: prompts and chunks written by position, several drafted tokens
+ * verified in one call, layers and contexts attended densely, and entries read back.
+ *
+ * A run is the new rows of a call: rows cu_rows[b] .. cu_rows[b+1] - 1 of the caller's arrays belong to
+ * sequence b of the batch and are its last n_b = cu_rows[b+1] - cu_rows[b] positions, so row t is position
+ * seq_len[b] - n_b + (t - cu_rows[b]) (seq_len counts them).  n_b may be 0.
+ *     cu_rows int32 [B+1] (device), 0 <= cu_rows[0] <= ... <= cu_rows[B] <= rows; n_b <= seq_len[b]
+ *     rows    host: rows of the caller's arrays, 0 <= rows <= CSA_MAX_SEQ_LEN; 0 is a no-op
+ * Rows outside [cu_rows[0], cu_rows[B]) of an output are left as they were.  Device metadata out of range
+ * (cu_rows, seq_len, a page id, an SWA row, a position without a rotation) is reported in ws; the rows it
+ * concerns are skipped, or the whole call where cu_rows is not ascending (csa_dense_attn).  Calls that
+ * overlap on the GPU, and captured graphs that may, need a workspace each.
+ *
+ * csa_kv_append_fp4 -- write a run into one layer's caches by position: the token's page and offset come
+ *   from the block table, its rotation from a table indexed by position, and the last 128 positions of
+ *   each sequence also go to its row of the window ring (swa_row -1, or layer->swa NULL: no window).
+ *     latent         bf16 [rows][512]; idx_key bf16 [rows][128]
+ *     norm_weight    float [512], or NULL: the latent is normalised already
+ *     rope_table     float [rope_positions][32][2] (cos, sin) of every position, or NULL: rotated already
+ *   RMSNorm, rotation, rounding to bf16 and pack are bit for bit those of csa_kv_norm_rope_pack_fp4 (with
+ *   both NULL, of csa_kv_pack_fp4).  ws needs CSA_WORKSPACE_HEADER_BYTES.
+ *
+ * csa_kv_unpack_fp4 -- the run's FP4 entries as values, latent bf16 [rows][512] = e2m1(code) * e4m3(scale)
+ *   (exact).  With n_b = seq_len[b] it reads a whole context.  ws needs CSA_WORKSPACE_HEADER_BYTES.
+ */
+csa_status csa_kv_append_fp4(const csa_kv_layer *layer, const csa_batch *batch, const int32_t *cu_rows, int32_t rows,
+                             const uint16_t *latent, const uint16_t *idx_key, const float *norm_weight,
+                             const float *rope_table, int32_t rope_positions, void *ws, size_t ws_bytes,
+                             void *stream);
+csa_status csa_kv_unpack_fp4(const csa_kv_layer *layer, const csa_batch *batch, const int32_t *cu_rows, int32_t rows,
+                             uint16_t *latent, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * csa_dense_attn -- attention of a run's query rows over every visible position of the FP4 cache (no
+ * selection, no window ring): for head h of row t at position p, over the positions j it sees,
+ *     s_j = sm_scale * q_h . v_j
+ *     s_j = softcap * tanh(s_j / softcap)      if softcap > 0
+ *     s_j = s_j - slopes[h] * |p - j|          if slopes
+ *     out_h = sum_j e^{s_j} v_j / sum_j e^{s_j},  lse_h = log sum_j e^{s_j}
+ *   q        bf16 [rows][H][512], 1 <= H <= 128
+ *   slopes   float [H] or NULL
+ *   spans    int32 [rows][2] or NULL: row t sees lo <= j < min(hi, seq_len), negative lo as 0; NULL is
+ *            causal, (0, p + 1).  A span holds a sliding window, the row's document in a packed sequence,
+ *            a prefix seen in both directions; one with lo >= hi sees nothing: out = 0, lse = -inf.
+ *   out      bf16 [rows][H][512], lse float [rows][H]
+ * fp16 operands (exact for the entries; q scaled by a power of two per row), fp32 accumulation and sums,
+ * probabilities rounded to fp16 once, out rounded to bf16 once.  Rows of non-finite q, and rows that see an
+ * entry with a NaN scale, give NaN; no other row does.  Results do not depend on timing, but rounding
+ * depends on how the call's rows divide over the GPU.  Every position of a bad page is left out.
+ * ws: csa_dense_attn_workspace_bytes() bytes, whatever the sizes.
+ */
+size_t csa_dense_attn_workspace_bytes(void);
+csa_status csa_dense_attn(const csa_kv_layer *layer, const csa_batch *batch, const int32_t *cu_rows, int32_t rows,
+                          const uint16_t *q, int32_t H, float sm_scale, float softcap, const float *slopes,
+                          const int32_t *spans, uint16_t *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
 /* Synchronise `stream`, read and clear the workspace status word.  Returns CSA_OK,
  * CSA_ERR_DEVICE_DATA or CSA_ERR_TIMEOUT; *detail (host, may be NULL) receives the first
  * offending index recorded. */
