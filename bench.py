@@ -135,7 +135,7 @@ def source_sha(names):
     return h.hexdigest()[:12]
 
 
-KERNEL_SOURCES = {"indexer_full": ["screen.cu", "select.cu", "score.cuh", "radix.cuh", "common.cuh", "convert.cuh",
+KERNEL_SOURCES = {"indexer_full": ["screen.cu", "tensor_map.cuh", "select.cu", "score.cuh", "radix.cuh", "common.cuh", "convert.cuh",
                                    "pipeline.cuh", "tcgen05.cuh"],
                   "indexer_reindex": ["indexer.cu", "score.cuh", "radix.cuh", "common.cuh", "convert.cuh",
                                       "pipeline.cuh"],

@@ -128,6 +128,26 @@ __device__ __forceinline__ void tc_ld16x32bx2_x16_pair(uint32_t ta, uint32_t tb,
     }
 }
 
+// 16 lanes x 64 columns with a half-warp split: thread i < 16 gets lane base+i, columns [col, col+32) and
+// thread i >= 16 lane base+i-16, columns [col+32, col+64); waited for in the same statement.
+__device__ __forceinline__ void tc_ld16x32bx2_x32(uint32_t taddr, float *v)
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // One arrival per warp: every lane's earlier writes (and its proxy or tcgen05 fences) are ordered
 // before lane 0's arrive by the warp barrier.  Barriers that warps arrive on count warps.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar)

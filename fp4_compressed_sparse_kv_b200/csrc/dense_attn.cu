@@ -5,103 +5,141 @@
 // the token index, dequantised in the kernel, in parallel); rebasdaily article on DeepSeek-V4.1-Flash KV
 // compression, section "同一份笔记，多层一起用" (FP4 main KV; the 512-channel latent is key and value).
 //
-// Row tile: 64 consecutive (token, head) rows of one sequence, token-major, so that 64 heads of one
-// decoded token, 16 heads of four drafted tokens or half of a 128-head token fill the same matrix
-// operand and any head count works.  Cache tile: one 64-position page.  For every (row tile, page):
-//   QK:  S_x[64 rows x 64 entries] = Q_x . V_x^T for the channel halves x = 0, 1 (M = 64; A = Q_x in
-//        TMEM, B = V K-major);
-//   PV:  O^T[128 ch x 64 rows] (x4) += V^T[128 ch x 64 entries] . P^T  (M = 128; A = V^T MN-major,
-//        B = P^T K-major).
-// The tile layout, TMEM columns, warp roles and numerics are those of attention_tc.cu (Q in TMEM, three
-// 64 KB fp16 V buffers, exact dequantisation, P rounded to fp16 once, fp32 accumulation and sums); Q is
-// scaled by a power of two per row, so a row of very large or non-finite values does not touch the
-// others of its tile.
+// Row tile: 128 consecutive (token, head) rows of one sequence, token-major, so that the 128 heads of one
+// token, 16 heads of eight drafted tokens or 64 heads of two prompt tokens fill the same matrix operand and
+// any head count works.  Cache tile: one 64-position page.  The fp32 output of 128 rows x 512 channels alone
+// would fill a TMEM, so a row tile belongs to a cluster of two CTAs, each with half of the channels: CTA x
+// dequantises channels 256x .. 256x+255 of a page (fp16, exact) and for every (row tile, page) computes
+//   QK:  S_x[128 rows x 64 entries] = Q_x . V_x^T     (M = 128, N = 64; A = Q_x in TMEM, B = V_x K-major);
+//   each CTA adds and exponentiates the two partial scores of half of the rows (half of S_x goes to the other
+//   CTA's shared memory, half of P comes back from there);
+//   PV:  O_x[128 rows x 256 ch] += P . V_x            (M = 128, N = 256; A = P K-major, B = V_x MN-major).
+// Every MMA runs at the tensor cores' full rate (M = 128), a page is dequantised once per 128 rows, and no
+// byte of V crosses between the CTAs.
+//
+// Numerics: fp16 operands (exact for the entries; P rounded to fp16 once), fp32 accumulation and sums.  Q is
+// scaled by a power of two per row and channel half, so a row of very large or non-finite values does not
+// touch the others of its tile.  O is rescaled only when a row's maximum has grown by 2^8.
 //
 // Work division: the (row tile, page) pairs of the whole call, row tile by row tile, are one line that
-// 148 persistent CTAs (one per SM) cut into equal shares, whatever the batch looks like: one long
-// sequence splits over all SMs, a prefill chunk gives each SM whole row tiles.  Every CTA works out the
-// division itself from cu_rows, seq_len and the spans (a block scan; no extra launch).  A CTA finishes
+// the 74 persistent clusters (one CTA per SM) cut into equal shares, whatever the batch looks like: one long
+// sequence splits over all SMs, a prefill chunk gives each cluster whole row tiles.  Every CTA works out the
+// division itself from cu_rows, seq_len and the spans (a block scan; no extra launch).  A cluster finishes
 // the row tiles it holds whole; the first and last tile of its share may be shared with its neighbours,
 // and those leave an fp32 partial (unnormalised O, running maximum and sum) in the workspace, which the
-// combine kernel adds in CTA order, so results do not depend on timing.
+// combine kernel adds in cluster order, so results do not depend on timing.
 #include <cuda_bf16.h>
 
 #include "attention_tile.cuh"
+#include "cluster.cuh"
 #include "convert.cuh"
 #include "dense_attn.cuh"
+#include "tensor_map.cuh"
 
 namespace csa {
 
 constexpr int kTile = 64;                        // entries per tile: one page
-constexpr int kDnChunks = kLatent / 64;          // 8 chunks of 64 channels
-constexpr int kDnStages = 3;                     // tiles in flight
-constexpr int kDnProducers = 512;                // warps 0-15
-constexpr int kDnSoftmax = 128;                  // warps 16-19
-constexpr int kDnSoftmaxWarp = 16;
-constexpr int kDnIssuerWarp = 20;                // warps 20-23
-constexpr int kDnThreads = 768;
-constexpr uint32_t kDnVChunk = kTile * 128;              // 8 KB: 64 rows x 64 fp16
-constexpr uint32_t kDnVBuf = kDnChunks * kDnVChunk;      // 64 KB per tile buffer
-constexpr uint32_t kDnPBuf = kDenseRows * 128;           // 8 KB: 64 rows x 64 entries fp16
+constexpr int kDnCh = kLatent / 2;               // channels of a CTA
+constexpr int kDnStages = 4;                     // V tiles in flight
+constexpr int kDnPStages = 2;                    // P tiles
+constexpr int kDnRawStages = 3;                  // tiles as the cache holds them
+constexpr int kDnFlags = 8;                      // tiles whose page is known to be valid or not
+constexpr int kDnGroups = 2;                     // tiles in their softmax at a time
+constexpr int kDnProducerWarps = 4;              // warps 0-3
+constexpr int kDnScoreWarp = 4;                  // warps 4-11: groups of four, one per TMEM quarter
+constexpr int kDnCorrWarp = kDnScoreWarp + 4 * kDnGroups;   // four warps, one per TMEM quarter
+constexpr int kDnQkWarp = kDnCorrWarp, kDnPvWarp = kDnCorrWarp + 1, kDnPlanWarp = kDnCorrWarp + 2;   // what else they do
+constexpr int kDnThreads = 32 * (kDnCorrWarp + 4);          // 128 registers each: a spill is a miss in the 20 KB of L1 left
+constexpr uint32_t kDnVChunk = kTile * 128;              // 8 KB: 64 entries x 64 fp16
+constexpr uint32_t kDnVBuf = kDnCh / 64 * kDnVChunk;     // 32 KB per tile buffer
+constexpr uint32_t kDnPBuf = kDenseRows * 128;           // 16 KB: 128 rows x 64 entries fp16
+constexpr uint32_t kDnRBuf = kDenseRows / 2 * kTile * 4; // 16 KB: 64 rows x 64 entries fp32
+constexpr uint32_t kDnRawCodes = kTile * kDnCh / 2;      // 8 KB: 64 entries x 256 channels of FP4
+constexpr uint32_t kDnRawScales = kTile * kDnCh / 16;    // 1 KB: their scales
 constexpr uint32_t kDnOffP = kDnStages * kDnVBuf;
-constexpr uint32_t kDnOffMisc = kDnOffP + kDnStages * kDnPBuf;
+constexpr uint32_t kDnOffR = kDnOffP + kDnPStages * kDnPBuf;
+constexpr uint32_t kDnOffC = kDnOffR + kDnGroups * kDnRBuf;
+constexpr uint32_t kDnOffSc = kDnOffC + kDnRawStages * kDnRawCodes;
+constexpr uint32_t kDnOffMisc = kDnOffSc + kDnRawStages * kDnRawScales;
 constexpr uint32_t kDnTmemCols = 512;
-constexpr uint32_t kDnColO = 0;                  // O^T: M-tile m in columns 64m .. 64m+63
-constexpr uint32_t kDnColQ = 256;                // Q_x: 128 columns in lane half x
-constexpr uint32_t kDnColS = 384;                // S_x of tile g: columns 384 + 64(g%2) in lane half x
-constexpr long long kDnMinTiles = 2;             // pages a CTA takes at least
+constexpr uint32_t kDnColO = 0;                  // O_x: 256 channels
+constexpr uint32_t kDnColQ = 256;                // Q_x: 256 channels, two per column
+constexpr uint32_t kDnColS = 384;                // S_x of tile g: columns 384 + 64(g%2) ..
+constexpr uint32_t kDnPBytes = kDenseRows / 2 * (128 + 4);   // of P and rescale factors, from the other CTA
+constexpr long long kDnMinTiles = 2;             // pages a cluster takes at least
+constexpr int kDnPieceCost = 8;                  // what a row tile costs besides its pages, in pages
 static_assert(kTile == kPage, "a tile is one page");
+static_assert(kDnStages * kDnVBuf >= kDenseRows * kDnCh * 2, "Q is staged in the V buffers");
 
-// One CTA's part of one row tile.
+// One cluster's part of one row tile.
 struct DensePiece {
     long long row;       // first row of the row tile over the call (token * H + head)
     uint32_t r0;         // the same within the sequence
-    int rows;            // rows of the row tile, 1 .. 64; 0: the CTA has no further piece
+    int rows;            // rows of the row tile, 1 .. 128; 0: the cluster has no further piece
     int b, c0, n, L;     // sequence, its first token, tokens and length
     int kv0, kv1;        // pages [kv0, kv1) of this piece; none if no row of the tile sees anything
     int first, last;     // the piece holds the first / last of the row tile's pages
 };
 
-// Where a CTA is on the line of (row tile, page) pairs.
+// Where a cluster is on the line of (row tile, page) pairs.
 struct DenseCursor {
     long long left;      // pairs of its share still to take
     long long off;       // pairs of row tile `tile` before them
     int tile, b;
 };
 
+// Tensor maps of the cache as [num_pages][64 entries][bytes]: boxes of 64 entries x one CTA's channels.
+struct DenseMaps {
+    CUtensorMap codes, scales;
+};
+
 struct DenseMisc {
-    uint64_t q_ready;
-    uint64_t v_ready[kDnStages], v_free[kDnStages], p_full[kDnStages];
+    DenseArgs args;
+    uint64_t raw_full[kDnRawStages], raw_free[kDnRawStages];
+    uint64_t v_ready[kDnStages], v_free[kDnStages];
     uint64_t s_full[2], s_free[2];
-    uint64_t final_bar[4];
-    uint64_t vmask[kDnStages];              // valid entries of the tile in each V buffer
-    uint32_t nan_tile[kDnStages];           // tile number + 1 if an entry of the tile has a NaN scale
-    uint32_t nan_entry[kDnStages][kTile];   // the same for each entry
+    uint64_t r_full[kDnGroups][4];          // scores received, by softmax warp
+    uint64_t r_free[kDnGroups][4];          // the other CTA has read those sent to it
+    uint64_t p_full[kDnPStages], p_free[kDnPStages], c_done[kDnPStages];
+    uint64_t m_full[kDnGroups][4];          // rows' references after a tile, by softmax warp
+    uint64_t inv_full;
+    uint64_t final_bar[2];
+    uint32_t nan_mask[kDnStages][kDnProducerWarps];    // entries with a NaN scale: bits of 32 entries per producer warp
+    int page_ok[kDnFlags];                             // the page id of tile g % 8 is valid
     uint32_t tmem_base;
     int abort_flag;
     long long warp_sum[kDnThreads / 32];
     DensePiece piece[2];
     DenseCursor cur;
     DenseShare share;
-    uint32_t qmax[kDenseRows];              // bits of each row's largest |q|
     float zs[kDenseRows];                   // accumulated score -> log2 domain, per row
-    float alpha[kDenseRows];                // rescale factor of each row at a maximum update
+    float m_row[kDnGroups][kDenseRows / 2]; // the references
+    float2 ml[kDnGroups][kDenseRows / 2];   // each group's reference and sum of p at the end of a piece
+    alignas(16) float alpha[kDnPStages][kDenseRows];   // rescale factor of each row before a tile
     float inv[kDenseRows];                  // 1 / denominator of a finished row
 };
 
 constexpr size_t kDnSmem = kDnOffMisc + sizeof(DenseMisc) + 1024;
-constexpr uint32_t kDnIdescQK = umma_idesc_f16(64, kTile, false, false);
-constexpr uint32_t kDnIdescPV = umma_idesc_f16(128, kDenseRows, true, false);
+constexpr uint32_t kDnIdescQK = umma_idesc_f16(kDenseRows, kTile, false, false);
+constexpr uint32_t kDnIdescPV = umma_idesc_f16(kDenseRows, kDnCh, false, true);
 
-// Named barriers: 1 = the softmax warps; 3 = the producers; 4 = every warp.
+// Named barriers: 1 + q = the score warps of quarter q.
+
+// Load of data that is read once: past the L1.
+__device__ __forceinline__ uint4 ld_stream16(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 
 // ------------------------------------------------------------------------------------------------
 // Work division.  Sequence b's row tiles have the numbers tile_base(b) .. tile_base(b + 1) - 1: at least
-// ceil(n_b H / 64) of them, the rest empty, without a scan over the batch.
+// ceil(n_b H / 128) of them, the rest empty, without a scan over the batch.
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ long long tile_base(int c0, int b, int H) { return (long long)c0 * H / kDenseRows + b; }
 
-// Pages [kv0, kv0 + nk) that rows r0 .. r0 + 63 of a sequence see between them.
+// Pages [kv0, kv0 + nk) that the rows of row tile r0 of a sequence see between them.
 __device__ __forceinline__ void tile_pages(const DenseArgs &a, int c0, int n, int L, uint32_t r0, int &kv0, int &nk)
 {
     const int ta = (int)(r0 / (uint32_t)a.H);
@@ -123,17 +161,17 @@ __device__ __forceinline__ void tile_pages(const DenseArgs &a, int c0, int n, in
     nk = hi > lo ? (hi + kPage - 1) / kPage - kv0 : 0;
 }
 
-// Share of the line that row tile r0 of a sequence takes: its pages, at least one so that a row tile
-// that sees nothing is written too; 0 for a tile number without rows or a sequence left out.
+// Share of the line that row tile r0 of a sequence takes: kDnPieceCost, then its pages; 0 for a tile number
+// without rows or a sequence left out.
 __device__ __forceinline__ int tile_weight(const DenseArgs &a, int c0, int n, int L, uint32_t r0)
 {
     if (L < n || r0 >= (uint32_t)n * (uint32_t)a.H) return 0;
     int kv0, nk;
     tile_pages(a, c0, n, L, r0, kv0, nk);
-    return max(nk, 1);
+    return kDnPieceCost + nk;
 }
 
-// The next piece of the CTA's share, and what the share leaves unfinished.
+// The next piece of the cluster's share, and what the share leaves unfinished.
 __device__ void next_piece(const DenseArgs &a, DenseCursor &cu, DenseShare &share, DensePiece &pc)
 {
     pc.rows = 0;
@@ -154,6 +192,12 @@ __device__ void next_piece(const DenseArgs &a, DenseCursor &cu, DenseShare &shar
         int kv0, nk;
         tile_pages(a, c0, n, L, r0, kv0, nk);
         const long long take = min((long long)w - cu.off, cu.left);
+        const int k0 = (int)max(0ll, cu.off - kDnPieceCost), k1 = (int)max(0ll, cu.off + take - kDnPieceCost);
+        const bool last = cu.off + take == w;
+        cu.left -= take;
+        cu.off = 0;
+        ++cu.tile;
+        if (k1 == k0 && !(nk == 0 && last)) continue;   // the share ends before the row tile's pages
         pc.row = (long long)c0 * a.H + r0;
         pc.r0 = r0;
         pc.rows = (int)min((uint32_t)kDenseRows, (uint32_t)n * (uint32_t)a.H - r0);
@@ -161,10 +205,10 @@ __device__ void next_piece(const DenseArgs &a, DenseCursor &cu, DenseShare &shar
         pc.c0 = c0;
         pc.n = n;
         pc.L = L;
-        pc.kv0 = kv0 + (int)cu.off;
-        pc.kv1 = min(kv0 + (int)(cu.off + take), kv0 + nk);
-        pc.first = cu.off == 0;
-        pc.last = cu.off + take == w;
+        pc.kv0 = kv0 + k0;
+        pc.kv1 = kv0 + k1;
+        pc.first = k0 == 0;
+        pc.last = last;
         if (!pc.first) {
             share.head = 1;
             share.head_ends = pc.last;
@@ -172,14 +216,11 @@ __device__ void next_piece(const DenseArgs &a, DenseCursor &cu, DenseShare &shar
             share.tail_row = pc.row;
             share.tail_rows = pc.rows;
         }
-        cu.left -= take;
-        cu.off = 0;
-        ++cu.tile;
         return;
     }
 }
 
-// This CTA's share: block-wide sums of the row tiles' weights, each thread over consecutive tiles, then
+// This cluster's share: block-wide sums of the row tiles' weights, each thread over consecutive tiles, then
 // the tile and page where the share begins.  `scratch` holds cu_rows and seq_len of every sequence.
 __device__ void plan(const DenseArgs &a, DenseMisc &ms, int32_t *scratch)
 {
@@ -239,10 +280,11 @@ __device__ void plan(const DenseArgs &a, DenseMisc &ms, int32_t *scratch)
         total += ms.warp_sum[i];
     }
     const long long excl = before + incl - sum;
-    // as many CTAs as leave each kDnMinTiles pages
-    const long long ctas = max(1ll, min((long long)gridDim.x, total / kDnMinTiles));
-    if (blockIdx.x < ctas) {
-        const long long s = total * blockIdx.x / ctas, e = total * (blockIdx.x + 1) / ctas;
+    // as many clusters as leave each kDnMinTiles pages
+    const long long pairs = max(1ll, min((long long)gridDim.x / 2, total / kDnMinTiles));
+    const int pair = blockIdx.x >> 1;
+    if (pair < pairs) {
+        const long long s = total * pair / pairs, e = total * (pair + 1) / pairs;
         if (s < e && excl <= s && s < excl + sum) {
             long long at = excl;
             b = b0;
@@ -260,47 +302,36 @@ __device__ void plan(const DenseArgs &a, DenseMisc &ms, int32_t *scratch)
 }
 
 // ------------------------------------------------------------------------------------------------
-// A producer thread's share of one page: entry e, channels 64cp .. 64cp+63 (V chunk cp).  The raw bytes
-// (32 B of codes, 4 scale bytes) are loaded into registers two tiles ahead and dequantised one tile
-// ahead, so that once PV releases the buffer only the stores remain.
+// A producer thread's share of one page: entry e, 128 channels (half cp of this CTA's).  TMA brings the raw
+// bytes, 64 B of codes (16-byte units swizzled as V's) and 8 scale bytes, three tiles ahead.
 // ------------------------------------------------------------------------------------------------
 struct PageEntry {
-    uint4 code[2];
-    uint32_t sc;
+    uint4 code[4];
+    uint2 sc;
     bool valid;
 
-    __device__ __forceinline__ void fetch(const DenseArgs &a, int page, bool ok, int e, int cp)
+    __device__ __forceinline__ void read(const uint8_t *codes, const uint8_t *scales, int e, int cp)
     {
-        valid = ok;
-        if (ok) {
-            const size_t row = (size_t)page * kPage + e;
-            const uint4 *c4 = reinterpret_cast<const uint4 *>(a.codes + row * kCodeBytes + 32 * cp);
-            code[0] = c4[0];
-            code[1] = c4[1];
-            sc = *reinterpret_cast<const uint32_t *>(a.scales + row * kScaleBytes + 4 * cp);
-        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = *reinterpret_cast<const uint4 *>(codes + swz((uint32_t)e, (uint32_t)(4 * cp + i)));
+        sc = *reinterpret_cast<const uint2 *>(scales + 16 * e + 8 * cp);
     }
 
-    // One of the four scales is NaN (E4M3 0x7F or 0xFF).
+    // One of the eight scales is NaN (E4M3 0x7F or 0xFF).
     __device__ __forceinline__ bool has_nan() const
     {
-        return valid && (((sc & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+        return valid && ((((sc.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sc.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u) != 0;
     }
 
-    // Channels 64cp .. 64cp+63 as 32 fp16 pairs; zeros for an invalid or NaN entry.
-    __device__ __forceinline__ void dequant(uint32_t *v) const
+    // Channels 64h .. 64h + 63 as 32 fp16 pairs; zeros for an invalid or NaN entry.
+    __device__ __forceinline__ void dequant(int h, bool ok, uint32_t *v) const
     {
-        if (!valid || has_nan()) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-            return;
-        }
         uint32_t sh[2];   // the four group scales as (s0, s1), (s2, s3)
-        e4m3x4_to_f16x2x2(sc, sh);
+        e4m3x4_to_f16x2x2(h ? sc.y : sc.x, sh);
 #pragma unroll
         for (int gg = 0; gg < 4; ++gg) {
             const uint32_t s2 = __byte_perm(sh[gg >> 1], 0u, (gg & 1) ? 0x3232u : 0x1010u);
-            const uint4 cw = code[gg >> 1];
+            const uint4 cw = code[2 * h + (gg >> 1)];
             uint32_t c0[4], c1[4];
             e2m1x8_to_f16x2x4((gg & 1) ? cw.z : cw.x, c0);
             e2m1x8_to_f16x2x4((gg & 1) ? cw.w : cw.y, c1);
@@ -310,96 +341,610 @@ struct PageEntry {
                 v[8 * gg + 4 + q] = hmul2_u32(c1[q], s2);
             }
         }
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
     }
 };
 
-// Q of the row tile into TMEM as the A operand of the QK MMAs, each row scaled by the power of two 2^k
-// that puts its largest |q| in [2^13, 2^14); ms.zs gets tau * log2(e) * 2^-k.  Warps 0-15; warp w writes
-// TMEM quarter w%4 (rows 16(w%4) .. +15) and channel block w/4 of each half: lane l converts channels
-// 256(l/16) + 64(w/4) .. +63 of row 16(w%4) + l%16 into 32 columns of lane 32(w%4) + l.  Rows past the
-// row tile's are zeros.
-__device__ __forceinline__ void load_q_rows(const DenseArgs &a, DenseMisc &ms, const DensePiece &pc, uint32_t tmem)
+// This CTA's channels of the row tile's Q into `stage`, each row scaled by the power of two 2^k that puts its
+// largest |q| of these channels in [2^13, 2^14), 16-byte units swizzled; ms.zs gets tau * log2(e) * 2^-k.
+// Warp w: the rows of lanes 8w .. 8w+7 (a row per load, 512 contiguous bytes); zeros past the row tile's rows.
+__device__ __forceinline__ void stage_q(const DenseArgs &a, DenseMisc &ms, const DensePiece &pc, int x, uint8_t *stage)
 {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, q = w & 3, j = w >> 2;
-    const int h = 16 * q + (lane & 15);
-    const int c0 = 256 * (lane >> 4) + 64 * j;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint4 qw[8];
-    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (size_t)(pc.row + h) * kLatent + c0);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) qw[c] = h < pc.rows ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-    uint32_t top = 0u;   // largest |q| as bf16 bits in the upper half
+    for (int j = 0; j < 8; ++j) {
+        const int r = 8 * w + j;
+        qw[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < pc.rows) qw[j] = ld_stream16(a.q + (size_t)(pc.row + r) * kLatent + kDnCh * x + 8 * lane);
+    }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const uint32_t ww[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
+    for (int j = 0; j < 8; ++j) {
+        const int i = 8 * w + j;
+        const uint32_t ww[4] = {qw[j].x, qw[j].y, qw[j].z, qw[j].w};
+        uint32_t top = 0u;   // largest |q| as bf16 bits in the upper half
 #pragma unroll
         for (int k = 0; k < 4; ++k) top = max(top, max(ww[k] & 0x7FFF0000u, (ww[k] << 16) & 0x7FFF0000u));
-    }
-    atomicMax(&ms.qmax[h], top);
-    bar_sync(3, kDnProducers);
-    top = ms.qmax[h];
-    int k = 0;
-    if (top != 0u) {
-        k = 13 - ((int)(top >> 23) - 127);
-        k = k < -120 ? -120 : (k > 120 ? 120 : k);
-    }
-    const float sc = exp2f((float)k);
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        uint32_t v[16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint4 x = qw[4 * hh + c];
-            v[4 * c] = pack_f16x2(bf16_lo(x.x) * sc, bf16_hi(x.x) * sc);
-            v[4 * c + 1] = pack_f16x2(bf16_lo(x.y) * sc, bf16_hi(x.y) * sc);
-            v[4 * c + 2] = pack_f16x2(bf16_lo(x.z) * sc, bf16_hi(x.z) * sc);
-            v[4 * c + 3] = pack_f16x2(bf16_lo(x.w) * sc, bf16_hi(x.w) * sc);
+        top = __reduce_max_sync(0xffffffffu, top);
+        int k = 0;
+        if (top != 0u) {
+            k = 13 - ((int)(top >> 23) - 127);
+            k = k < -120 ? -120 : (k > 120 ? 120 : k);
         }
-        tc_st16_u(tmem + ((uint32_t)(32 * q) << 16) + kDnColQ + 32 * j + 16 * hh, v);
+        const float sc = exp2f((float)k);
+        uint32_t h[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) h[m] = pack_f16x2(bf16_lo(ww[m]) * sc, bf16_hi(ww[m]) * sc);
+        *reinterpret_cast<uint4 *>(stage + i * 512 + ((lane ^ (i & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (lane == 0) ms.zs[i] = a.sm_scale * exp2f((float)-k) * kLog2e;
     }
-    tc_wait_st();
-    tc_fence_before();
-    if (j == 0 && lane < 16) ms.zs[h] = a.sm_scale * exp2f((float)-k) * kLog2e;
-    warp_arrive(&ms.q_ready);
 }
 
-__global__ void __launch_bounds__(kDnThreads, 1) dense_attn_kernel(DenseArgs a)
+// The staged rows into TMEM as the A operand of the QK MMAs: warp w stores quarter w%4, channels 64(w/4) ..
+__device__ __forceinline__ void store_q(const uint8_t *stage, uint32_t tmem)
+{
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int q = w & 3, cg = w >> 2, i = 32 * q + lane;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t v[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int unit = 8 * cg + 4 * j + k;
+            const uint4 y = *reinterpret_cast<const uint4 *>(stage + i * 512 + ((unit ^ (i & 7)) << 4));
+            v[4 * k] = y.x;
+            v[4 * k + 1] = y.y;
+            v[4 * k + 2] = y.z;
+            v[4 * k + 3] = y.w;
+        }
+        tc_st16_u(tmem + ((uint32_t)(32 * q) << 16) + kDnColQ + 32 * cg + 16 * j, v);
+    }
+    tc_wait_st();
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint8_t *dense_smem()
 {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *V = base;
-    uint8_t *P = base + kDnOffP;
-    DenseMisc &ms = *reinterpret_cast<DenseMisc *>(base + kDnOffMisc);
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
+
+__device__ __forceinline__ DenseMisc &dense_misc(uint8_t *base) { return *reinterpret_cast<DenseMisc *>(base + kDnOffMisc); }
+
+// ------------------------------------------------------------------------------------------------
+// Roles of the warps while a piece runs.  Each is a function of its own: the register allocation of one
+// does not see what the others keep, and nothing is spilled inside a tile loop (the L1 beside 200 KB of
+// shared memory holds no stack: a reload costs an L2 access).  They return false after a failed wait.
+// ------------------------------------------------------------------------------------------------
+// Rescaling of O, MMA issue, next piece.
+__device__ __noinline__ bool dense_mma(int pi, uint32_t g0)
+{
+    uint8_t *base = dense_smem();
+    DenseMisc &ms = dense_misc(base);
+    const DenseArgs &a = ms.args;
+    const DensePiece &pc = ms.piece[pi];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WaitCtx cx{&ms.abort_flag, a.ws};
+    const uint32_t tmem = ms.tmem_base;
+    const int nk = pc.kv1 - pc.kv0;
+    bool ok = true;
+    uint8_t *V = base, *P = base + kDnOffP;
+    const int q = warp & 3;
+    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + kDnColO;
+    const uint32_t sV = smem_addr(V), sP = smem_addr(P);
+    // QK into S of tile g (columns of parity g % 2) once the producers have written the tile and the
+    // score warps have read tile g - 2's scores
+    auto issue_qk = [&](int t) {
+        const uint32_t g = g0 + t, p = g % kDnStages, sb = g & 1u;
+        if (!warp_wait_hint(&ms.v_ready[p], (g / kDnStages) & 1u, cx, 3)) return false;
+        if (g >= 2 && !warp_wait_hint(&ms.s_free[sb], ((g >> 1) - 1u) & 1u, cx, 10)) return false;
+        if (lane == 0) {
+            tc_fence_after();
+#pragma unroll 4
+            for (int k = 0; k < kDnCh / 16; ++k) {
+                const uint64_t bd = umma_sdesc_sw128(sV + p * kDnVBuf + (k >> 2) * kDnVChunk + (k & 3) * 32, 16, 1024);
+                tc_mma_f16_ts(tmem + kDnColS + 64 * sb, tmem + kDnColQ + 8 * k, bd, kDnIdescQK, k > 0 ? 1u : 0u);
+            }
+            tc_commit(smem_addr(&ms.s_full[sb]));
+        }
+        __syncwarp();
+        return true;
+    };
+    if (lane == 0 && warp == kDnPlanWarp) next_piece(a, ms.cur, ms.share, ms.piece[pi ^ 1]);
+    __syncwarp();
+#pragma unroll 1
+    for (int t = -2; ok && t < nk; ++t) {
+        if (warp == kDnQkWarp && t + 2 < nk) {
+            ok = issue_qk(t + 2);
+            if (!ok) break;
+        }
+        if (t < 0) continue;
+        const uint32_t g = g0 + t, p = g % kDnStages, pp = g % kDnPStages;
+        ok = warp_wait_hint(&ms.p_full[pp], (g / kDnPStages) & 1u, cx, 7);
+        if (!ok) break;
+        const float al = ms.alpha[pp][32 * q + lane];
+        if (t > 0 && 32 * q < pc.rows && __any_sync(0xffffffffu, al != 1.f)) {
+            // some row's maximum grew: this warp's rows of O, once PV of the previous tile has completed
+            const uint32_t gp = g - 1u;
+            ok = warp_wait_hint(&ms.v_free[gp % kDnStages], (gp / kDnStages) & 1u, cx, 13);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < kDnCh; k += 32) {
+                float o[32];
+                tc_ld32_sync(tq + k, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= al;
+                tc_st32(tq + k, o);
+            }
+            tc_wait_st();
+            tc_fence_before();
+        }
+        __syncwarp();
+        lane0_arrive(&ms.c_done[pp], lane);
+        if (warp == kDnPvWarp) {
+            // PV once O is at its scale; the commits release the tile's V buffer and, in both CTAs, its
+            // P buffer
+            ok = warp_wait_hint(&ms.c_done[pp], (g / kDnPStages) & 1u, cx, 12);
+            if (!ok) break;
+            if (lane == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk) {
+                    const uint64_t ad = umma_sdesc_sw128(sP + pp * kDnPBuf + kk * 32, 16, 1024);
+                    const uint64_t bd = umma_sdesc_sw128(sV + p * kDnVBuf + kk * 2048, kDnVChunk, 1024);
+                    tc_mma_f16(tmem + kDnColO, ad, bd, kDnIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
+                }
+                tc_commit_both(smem_addr(&ms.p_free[pp]));
+                tc_commit(smem_addr(&ms.v_free[p]));
+            }
+            __syncwarp();
+        }
+    }
+    return ok;
+}
+
+// Page of tile t of a piece to shared memory, by warp 0; `ids` holds the page ids of tiles t & ~31 ..
+__device__ __forceinline__ void dense_fetch(const DenseArgs &a, DenseMisc &ms, const DenseMaps *maps, uint8_t *base, int ids, int t,
+                                            uint32_t g, int kv0)
+{
+    const int lane = threadIdx.x & 31, page = __shfl_sync(0xffffffffu, ids, t & 31);
+    if (lane == 0) {
+        const uint32_t st = g % kDnRawStages;
+        const bool ok = page >= 0 && page < a.num_pages;
+        ms.page_ok[g % kDnFlags] = ok;
+        if (ok) {
+            mbar_arrive_expect_tx(&ms.raw_full[st], kDnRawCodes + kDnRawScales);
+            const int x = (int)cluster_rank();
+            tma_load_3d(smem_addr(base + kDnOffC + st * kDnRawCodes), &maps->codes, 128 * x, 0, page, &ms.raw_full[st]);
+            tma_load_3d(smem_addr(base + kDnOffSc + st * kDnRawScales), &maps->scales, 16 * x, 0, page, &ms.raw_full[st]);
+        } else {
+            report(a.ws, CSA_ERR_DEVICE_DATA, kv0 + t);
+            mbar_arrive(&ms.raw_full[st]);
+        }
+    }
+    __syncwarp();
+}
+
+// The first two pages of a piece, ahead of everything else (warp 0).
+__device__ __forceinline__ void dense_prefetch(const DenseArgs &a, DenseMisc &ms, const DenseMaps *maps, uint8_t *base,
+                                               const DensePiece &pc, uint32_t g0)
+{
+    const int nk = pc.kv1 - pc.kv0, lane = threadIdx.x & 31;
+    const int ids = lane < nk ? a.block_table[(size_t)pc.b * a.max_pages + pc.kv0 + lane] : -1;
+    for (int t = 0; t < min(nk, 2); ++t) dense_fetch(a, ms, maps, base, ids, t, g0 + t, pc.kv0);
+}
+
+// Pages of the piece, dequantised, into the V buffers.
+__device__ __noinline__ bool dense_produce(int pi, uint32_t g0, const DenseMaps *maps)
+{
+    uint8_t *base = dense_smem();
+    DenseMisc &ms = dense_misc(base);
+    const DenseArgs &a = ms.args;
+    const DensePiece &pc = ms.piece[pi];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WaitCtx cx{&ms.abort_flag, a.ws};
+    const int nk = pc.kv1 - pc.kv0, kv0 = pc.kv0;
+    const int32_t *bt = a.block_table + (size_t)pc.b * a.max_pages + kv0;
+    const int left = pc.L - kv0 * kPage;   // positions of the sequence from the piece's first page on
+    const int e = tid & (kTile - 1), cp = tid >> 6;
+    int ids = lane < nk ? bt[lane] : -1, ids_next = 32 + lane < nk ? bt[32 + lane] : -1;
+    bool ok = true;
+#pragma unroll 1
+    for (int t = 0; ok && t < nk; ++t) {
+        const uint32_t g = g0 + t, p = g % kDnStages, st = g % kDnRawStages;
+        if (warp == 0 && t + 2 < nk) {
+            const uint32_t gf = g + 2;
+            if (gf >= kDnRawStages) ok = warp_wait_hint(&ms.raw_free[gf % kDnRawStages], (gf / kDnRawStages - 1u) & 1u, cx, 20);
+            if (!ok) break;
+            if (((t + 2) & 31) == 0) {
+                ids = ids_next;
+                ids_next = t + 34 + lane < nk ? bt[t + 34 + lane] : -1;
+            }
+            dense_fetch(a, ms, maps, base, ids, t + 2, gf, kv0);
+        }
+        ok = warp_wait_hint(&ms.raw_full[st], (g / kDnRawStages) & 1u, cx, 21);
+        if (!ok) break;
+        PageEntry raw;
+        raw.read(base + kDnOffC + st * kDnRawCodes, base + kDnOffSc + st * kDnRawScales, e, cp);
+        raw.valid = ms.page_ok[g % kDnFlags] && t * kPage + e < left;
+        __syncwarp();
+        lane0_arrive(&ms.raw_free[st], lane);
+        const bool is_nan = raw.has_nan(), use = raw.valid && !is_nan;
+        const unsigned int nan = __ballot_sync(0xffffffffu, is_nan);
+        if (g >= kDnStages) ok = warp_wait_hint(&ms.v_free[p], (g / kDnStages - 1u) & 1u, cx, 5);
+        if (!ok) break;
+        uint8_t *dst = base + p * kDnVBuf + 2 * cp * kDnVChunk;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            raw.dequant(h, use, v);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4 *>(dst + h * kDnVChunk + swz((uint32_t)e, (uint32_t)u)) =
+                    make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        }
+        if (lane == 0) ms.nan_mask[p][warp] = nan;
+        fence_async_smem();
+        __syncwarp();
+        lane0_arrive(&ms.v_ready[p], lane);
+    }
+    return ok;
+}
+
+// Scores and softmax.
+__device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
+{
+    uint8_t *base = dense_smem();
+    DenseMisc &ms = dense_misc(base);
+    const DenseArgs &a = ms.args;
+    const DensePiece &pc = ms.piece[pi];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int x = (int)cluster_rank();
+    const WaitCtx cx{&ms.abort_flag, a.ws};
+    const uint32_t tmem = ms.tmem_base;
+    const int nk = pc.kv1 - pc.kv0;
+    bool ok = true;
+    uint8_t *P = base + kDnOffP, *R = base + kDnOffR;
+    const uint32_t peer = (uint32_t)(x ^ 1);
+    uint32_t sent = n_sent;
+    // Warp (group a, quarter q) takes the tiles g with g % kDnGroups == a.  In its TMEM quarter lanes 16y ..
+    // 16y + 15 are rows of CTA y: it sends the other CTA's 16 rows of partial scores there and does the softmax
+    // of its own 16, thread i < 16 entries 0-31 of row i, thread 16 + i entries 32-63.
+    const int q = warp & 3, grp = (warp - kDnScoreWarp) >> 2;
+    const int u = lane >> 4;
+    const int hl = 32 * q + 16 * x + (lane & 15);   // this thread's TMEM lane and row of the row tile
+    const int hr = 16 * q + (lane & 15);            // row among this CTA's
+    const bool active = 32 * q < pc.rows;           // the quarter has rows (the same in both CTAs)
+    const uint32_t ts = tmem + ((uint32_t)(32 * q + 16 * x) << 16) + kDnColS;
+    const uint32_t to = tmem + ((uint32_t)(32 * q + 16 * (x ^ 1)) << 16) + kDnColS;
+    const float zs = ms.zs[hl], zo = ms.zs[hl ^ 16];
+    const uint32_t row = pc.r0 + (uint32_t)hl;
+    const int tok = (int)(row / (uint32_t)a.H);
+    const int pos = pc.L - pc.n + tok;
+    int lo = 0, hi = 0;                      // positions the row sees
+    float slope = 0.f;                       // of the distance bias, log2 domain
+    if (hl < pc.rows) {
+        hi = pos + 1;
+        if (a.spans) {
+            const int2 s = a.spans[pc.c0 + tok];
+            lo = max(s.x, 0);
+            hi = min(s.y, pc.L);
+        }
+        if (a.slopes) slope = a.slopes[row - (uint32_t)tok * (uint32_t)a.H] * kLog2e;
+    }
+    const uint32_t pr = remote_addr(smem_addr(P), peer);
+    const uint32_t rr = remote_addr(smem_addr(R) + kDnRBuf * grp + 4096u * q + 16u * lane, peer);
+    const uint4 *rbuf = reinterpret_cast<const uint4 *>(R + kDnRBuf * grp + 4096 * q) + lane;
+    float m_run = kNoMax;                    // the reference of this thread's sum (log2 domain)
+    float lsum = 0.f;                        // its share of the row's denominator
+#pragma unroll 1
+    for (int t = (int)((uint32_t)(grp + kDnGroups - (int)(g0 % kDnGroups)) % kDnGroups); t < nk; t += kDnGroups) {
+        const uint32_t g = g0 + t, p = g % kDnStages, sb = g & 1u, pp = g % kDnPStages;
+        if (active) lane0_arrive_expect_tx(&ms.r_full[grp][q], 4096u, lane);
+        ok = ok && warp_wait_hint(&ms.v_ready[p], (g / kDnStages) & 1u, cx, 9) &&
+             warp_wait_hint(&ms.s_full[sb], (g >> 1) & 1u, cx, 6);
+        if (ok && active && sent > 0) ok = warp_wait_hint(&ms.r_free[grp][q], (sent - 1u) & 1u, cx, 14);
+        if (!ok) break;
+        const uint32_t nan = ms.nan_mask[p][u] | ms.nan_mask[p][2 + u];   // entries with a NaN scale in this CTA's channels
+        const bool page_ok = ms.page_ok[g % kDnFlags];
+        float z[32];
+        tc_fence_after();
+        if (active) {
+            tc_ld16x32bx2_x32(to + 64 * sb, z);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] *= zo;
+            if (nan) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if ((nan >> i) & 1u) z[i] = __int_as_float(0x7FC00000);
+            }
+            const uint32_t rb = remote_addr(smem_addr(&ms.r_full[grp][q]), peer);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                st_async16(rr + 512u * i,
+                           make_uint4(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]),
+                                      __float_as_uint(z[4 * i + 2]), __float_as_uint(z[4 * i + 3])),
+                           rb);
+            tc_ld16x32bx2_x32(ts + 64 * sb, z);
+        }
+        tc_fence_before();
+        __syncwarp();
+        lane0_arrive(&ms.s_free[sb], lane);   // QK of tile g + 2 may overwrite these columns
+        float al = 1.f;
+        if (active) {
+            ok = warp_wait_hint(&ms.r_full[grp][q], sent & 1u, cx, 15);
+            ++sent;
+            if (!ok) break;
+            // z = both halves of the channels, log2 domain
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 o = rbuf[32 * i];
+                z[4 * i] = fmaf(z[4 * i], zs, __uint_as_float(o.x));
+                z[4 * i + 1] = fmaf(z[4 * i + 1], zs, __uint_as_float(o.y));
+                z[4 * i + 2] = fmaf(z[4 * i + 2], zs, __uint_as_float(o.z));
+                z[4 * i + 3] = fmaf(z[4 * i + 3], zs, __uint_as_float(o.w));
+            }
+            __syncwarp();
+            lane0_arrive_remote(remote_addr(smem_addr(&ms.r_free[grp][q]), peer), lane);
+            const int e0 = (pc.kv0 + t) * kPage + 32 * u;   // position of z[0]
+            if (a.softcap > 0.f) {
+                // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap))): absolute error a few 2^-24 cap
+                const float arg = 2.f / a.softcap, cap = a.softcap * kLog2e;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = cap * (1.f - __fdividef(2.f, 1.f + exp2f(z[i] * arg)));
+            }
+            if (a.slopes) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = fmaf(-slope, fabsf((float)(pos - e0 - i)), z[i]);
+            }
+            if (nan) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if ((nan >> i) & 1u) z[i] = __int_as_float(0x7FC00000);
+            }
+            // entries of a mapped page that the row sees
+            uint32_t seen = page_ok ? 0xFFFFFFFFu : 0u;
+            if (lo > e0) seen &= lo - e0 < 32 ? 0xFFFFFFFFu << (lo - e0) : 0u;
+            if (hi < e0 + 32) seen &= hi > e0 ? 0xFFFFFFFFu >> (32 - (hi - e0)) : 0u;
+            if (seen != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (!((seen >> i) & 1u)) z[i] = -INFINITY;
+            }
+            float mt = z[0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) mt = fmaxf(mt, z[i]);
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
+            // the row's reference after the previous tile, which another group has; it grows only by more
+            // than 2^8 at a time
+            float m_old = kNoMax;
+            if (t > 0) {
+                const uint32_t gp = g - 1u;
+                ok = warp_wait_hint(&ms.m_full[gp % kDnGroups][q], (gp / kDnGroups) & 1u, cx, 18);
+                if (!ok) break;
+                m_old = ms.m_row[gp % kDnGroups][hr];
+            }
+            const float m_new = mt > m_old + kLazy ? fmaxf(m_old, mt) : m_old;
+            if (u == 0) ms.m_row[grp][hr] = m_new;
+            __syncwarp();
+            lane0_arrive(&ms.m_full[grp][q], lane);
+            al = ex2(m_old - m_new);        // 0 while m_old is kNoMax, 1 if unchanged
+            lsum *= ex2(m_run - m_new);
+            m_run = m_new;
+        } else {                            // the barrier's phases count tiles
+            lane0_arrive(&ms.m_full[grp][q], lane);
+        }
+        if (g >= kDnPStages) ok = warp_wait_hint(&ms.p_free[pp], (g / kDnPStages - 1u) & 1u, cx, 16);
+        if (!ok) break;
+        if (active) {
+            // P row hl, entries 32u .. 32u+31, here and in the other CTA: four 16-byte units of the
+            // 128-byte swizzled row; p = 2^(z - m + 7), 0 for a masked entry (z = -inf)
+            const float mref = m_run - kPOffset;
+            const uint32_t pf = remote_addr(smem_addr(&ms.p_full[pp]), peer);
+            float ls = 0.f;
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p0 = ex2(z[8 * gq + 2 * i] - mref);
+                    const float p1 = ex2(z[8 * gq + 2 * i + 1] - mref);
+                    ls += p0 + p1;
+                    pk[i] = pack_f16x2(p0, p1);
+                }
+                const uint4 w = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                const uint32_t at = pp * kDnPBuf + swz((uint32_t)hl, (uint32_t)(4 * u + gq));
+                *reinterpret_cast<uint4 *>(P + at) = w;
+            }
+            if (u == 0) ms.alpha[pp][hl] = al;
+            lsum += ls;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                // the 16 rows are contiguous: one copy of 2 KB (16-byte stores to 16 rows cost twice the time and
+                // slow every other access of the shared memory)
+                const uint32_t r16 = 32u * q + 16u * x;
+                bulk_to_cta(pr + pp * kDnPBuf + 128u * r16, smem_addr(P) + pp * kDnPBuf + 128u * r16, 2048u, pf);
+                bulk_to_cta(remote_addr(smem_addr(&ms.alpha[pp][r16]), peer), smem_addr(&ms.alpha[pp][r16]), 64u, pf);
+            }
+        }
+        __syncwarp();
+        if (active) lane0_arrive_expect_tx(&ms.p_full[pp], kDnPBytes / 4, lane);
+        else lane0_arrive(&ms.p_full[pp], lane);
+    }
+    // the row's denominator from its two threads of every group
+    lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+    if (u == 0) ms.ml[grp][hr] = make_float2(m_run, lsum);
+    bar_sync(1 + q, 32 * kDnGroups);
+    if (grp == 0) {
+        float M = kNoMax, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kDnGroups; ++i) M = fmaxf(M, ms.ml[i][hr].x);
+#pragma unroll
+        for (int i = 0; i < kDnGroups; ++i) l += ex2(ms.ml[i][hr].x - M) * ms.ml[i][hr].y;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (u == 0) {
+            if (hl < pc.rows) {
+                // a row that sees nothing: out = 0, lse = -inf (a NaN sum stays NaN)
+                if (pc.first && pc.last)
+                    a.lse[pc.row + hl] = l == 0.f ? -INFINITY : (M - kPOffset) * kLn2 + logf(l);
+                else
+                    a.part_ml[(size_t)(2 * (blockIdx.x >> 1) + (pc.first ? 1 : 0)) * kDenseRows + hl] = make_float2(M - kPOffset, l);
+            }
+            if (nk > 0 && ok) {
+                ms.inv[hl] = inv;
+                st_async4(remote_addr(smem_addr(&ms.inv[hl]), peer), __float_as_uint(inv),
+                          remote_addr(smem_addr(&ms.inv_full), peer));
+            }
+        }
+        __syncwarp();
+        if (nk > 0) lane0_arrive_expect_tx(&ms.inv_full, 64u, lane);
+    }
+    n_sent = sent;
+    return ok;
+}
+
+// O of the piece to out or to a partial: quarter w%4, channels 64(w/4) .. of this CTA's, each warp through 4 KB
+// of the V buffers so that its stores are whole rows of 128 bytes.
+__device__ __noinline__ bool dense_epilogue(int pi, uint32_t g0, uint32_t pieces, bool ok)
+{
+    uint8_t *base = dense_smem();
+    DenseMisc &ms = dense_misc(base);
+    const DenseArgs &a = ms.args;
+    const DensePiece &pc = ms.piece[pi];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int x = (int)cluster_rank();
+    const WaitCtx cx{&ms.abort_flag, a.ws};
+    const uint32_t tmem = ms.tmem_base;
+    const int nk = pc.kv1 - pc.kv0;
+    uint8_t *V = base;
+    if (nk > 0) {
+        const uint32_t gl = g0 + nk - 1;
+        ok = ok && warp_wait_hint(&ms.v_free[gl % kDnStages], (gl / kDnStages) & 1u, cx, 8) &&
+             warp_wait_hint(&ms.inv_full, pieces & 1u, cx, 17);
+    }
+    // the V buffers are free once every warp that reads or writes them has come here
+    if (__syncthreads_and(ok)) {
+        tc_fence_after();
+        const int q = warp & 3, c0 = 64 * (warp >> 2), r0 = 32 * q;
+        const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kDnColO + c0;
+        uint8_t *st = V + 4096 * warp;
+        const bool whole = pc.first && pc.last;
+        const float inv = ms.inv[32 * q + lane];
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            float o[32];
+            if (nk > 0) {
+                tc_ld32_sync(to + 32 * h, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+            if (whole) {
+                const float sc = nk > 0 ? inv : 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t b[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(o[8 * i + 2 * j] * sc, o[8 * i + 2 * j + 1] * sc);
+                        b[j] = *reinterpret_cast<const uint32_t *>(&y);
+                    }
+                    *reinterpret_cast<uint4 *>(st + swz((uint32_t)lane, (uint32_t)(4 * h + i))) = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+                if (h == 0) continue;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4 *>(st + swz((uint32_t)lane, (uint32_t)i)) =
+                        make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+            __syncwarp();
+            // row r0 + l of 128 bytes: eight lanes
+            const int unit = lane & 7;
+            uint8_t *dst = whole ? reinterpret_cast<uint8_t *>(a.out + (size_t)(pc.row + r0) * kLatent + kDnCh * x + c0)
+                                 : reinterpret_cast<uint8_t *>(a.part_o +
+                                       ((size_t)(2 * (blockIdx.x >> 1) + (pc.first ? 1 : 0)) * kDenseRows + r0) * kLatent +
+                                       kDnCh * x + c0 + 32 * h);
+            const uint32_t stride = whole ? 2 * kLatent : 4 * kLatent;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int l = 4 * i + (lane >> 3);
+                if (r0 + l < pc.rows)
+                    *reinterpret_cast<uint4 *>(dst + (size_t)l * stride + 16 * unit) =
+                        *reinterpret_cast<const uint4 *>(st + swz((uint32_t)l, (uint32_t)unit));
+            }
+            __syncwarp();
+        }
+    }
+    return ok;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
+    dense_attn_kernel(const __grid_constant__ DenseMaps maps, DenseArgs a)
+{
+    uint8_t *V = dense_smem();
+    DenseMisc &ms = dense_misc(V);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int x = (int)cluster_rank();
     grid_dep_launch();   // the combine may be scheduled as CTAs finish
 
     if (tid == 0) {
-        mbar_init(&ms.q_ready, kDnProducers / 32);
+        for (int i = 0; i < kDnRawStages; ++i) {
+            mbar_init(&ms.raw_full[i], 1);
+            mbar_init(&ms.raw_free[i], kDnProducerWarps);
+        }
         for (int i = 0; i < kDnStages; ++i) {
-            mbar_init(&ms.v_ready[i], kDnProducers / 32);
-            mbar_init(&ms.v_free[i], 2);
-            mbar_init(&ms.p_full[i], kDnSoftmax / 32);
-            ms.nan_tile[i] = 0;
+            mbar_init(&ms.v_ready[i], kDnProducerWarps);
+            mbar_init(&ms.v_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ms.s_full[i], 2);
-            mbar_init(&ms.s_free[i], kDnSoftmax / 32);
+            mbar_init(&ms.s_full[i], 1);
+            mbar_init(&ms.s_free[i], 4);
         }
-        for (int r = 0; r < 4; ++r) mbar_init(&ms.final_bar[r], 1);
+        for (int i = 0; i < kDnGroups; ++i)
+            for (int w = 0; w < 4; ++w) {
+                mbar_init(&ms.r_full[i][w], 1);
+                mbar_init(&ms.r_free[i][w], 1);
+            }
+        for (int i = 0; i < kDnPStages; ++i) {
+            mbar_init(&ms.p_full[i], 4);
+            mbar_init(&ms.p_free[i], 2);
+            mbar_init(&ms.c_done[i], 4);
+        }
+        for (int i = 0; i < kDnGroups; ++i)
+            for (int w = 0; w < 4; ++w) mbar_init(&ms.m_full[i][w], 1);
+        mbar_init(&ms.inv_full, 4);
+        for (int r = 0; r < 2; ++r) mbar_init(&ms.final_bar[r], 1);
         ms.abort_flag = 0;
+        ms.args = a;
         fence_mbar_init();
     }
-    if (tid < kDenseRows) ms.qmax[tid] = 0u;
-    if (tid < kDnStages * kTile) (&ms.nan_entry[0][0])[tid] = 0u;
-    if (warp == kDnIssuerWarp) {
+    if (warp == kDnQkWarp) {
         tc_alloc(smem_addr(&ms.tmem_base), kDnTmemCols);
         tc_relinquish();
     }
-    grid_dep_wait();   // everything below reads what earlier kernels wrote, or writes what they read
+    grid_dep_wait();     // everything below reads what earlier kernels wrote, or writes what they read
     plan(a, ms, reinterpret_cast<int32_t *>(V));
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();      // the other CTA's barriers are there, and it has read its plan from where P goes
 
+    const WaitCtx cx{&ms.abort_flag, a.ws};
     bool ok = true;
     uint32_t g0 = 0;      // tiles of the earlier pieces
     uint32_t pieces = 0;  // earlier pieces that had tiles
+    uint32_t sent = 0;    // score warps: tiles whose scores went to the other CTA (and came from there)
     for (int pi = 0;; pi ^= 1) {
         // the piece is visible and the previous one is finished with TMEM and shared memory
         tc_fence_before();
@@ -409,330 +954,77 @@ __global__ void __launch_bounds__(kDnThreads, 1) dense_attn_kernel(DenseArgs a)
         if (pc.rows == 0) break;
         const uint32_t tmem = ms.tmem_base;
         const int nk = pc.kv1 - pc.kv0;
-
-        if (warp >= kDnIssuerWarp) {
-            // ------------------------------- MMA issuers -------------------------------
-            const int r = warp - kDnIssuerWarp;
-            if (r == 3 && lane == 0) next_piece(a, ms.cur, ms.share, ms.piece[pi ^ 1]);
-            if (lane == 0 && nk > 0) {
-                const uint32_t sV = smem_addr(V), sP = smem_addr(P);
-                ok = mbar_wait(&ms.q_ready, pieces & 1u, &ms.abort_flag, a.ws, 1);
-                tc_fence_after();
-                if (r < 2) {
-                    // QK of channel half r into S_r of tile g (lanes of half r, columns of parity g % 2),
-                    // once the producers have written the tile and the softmax has read tile g - 2's scores
-                    const uint32_t lanes = (uint32_t)(16 * r) << 16;
-                    for (int t = 0; ok && t < nk; ++t) {
-                        const uint32_t g = g0 + t, p = g % kDnStages, sb = g & 1u;
-                        ok = mbar_wait(&ms.v_ready[p], (g / kDnStages) & 1u, &ms.abort_flag, a.ws, 3);
-                        if (ok && g >= 2) ok = mbar_wait(&ms.s_free[sb], ((g >> 1) - 1u) & 1u, &ms.abort_flag, a.ws, 10);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int c = 4 * r + (k >> 2);   // V chunk of channels 256r + 16k ..
-                            const uint64_t bd = umma_sdesc_sw128(sV + p * kDnVBuf + c * kDnVChunk + (k & 3) * 32, 16, 1024);
-                            tc_mma_f16_ts(tmem + lanes + kDnColS + 64 * sb, tmem + lanes + kDnColQ + 8 * k, bd, kDnIdescQK,
-                                          k > 0 ? 1u : 0u);
-                        }
-                        tc_commit(smem_addr(&ms.s_full[sb]));
-                    }
-                } else {
-                    // PV of M-tiles 2(r-2), 2(r-2)+1 once the softmax has written P of the tile; the commit
-                    // releases the tile's V and P buffers
-                    const int m0 = 2 * (r - 2);
-                    for (int t = 0; ok && t < nk; ++t) {
-                        const uint32_t g = g0 + t, p = g % kDnStages;
-                        ok = mbar_wait(&ms.p_full[p], (g / kDnStages) & 1u, &ms.abort_flag, a.ws, 2);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-                            for (int kk = 0; kk < kTile / 16; ++kk) {
-                                const int m = m0 + mi;
-                                const uint64_t ad = umma_sdesc_sw128(sV + p * kDnVBuf + 2 * m * kDnVChunk + kk * 2048, kDnVChunk, 1024);
-                                const uint64_t bd = umma_sdesc_sw128(sP + p * kDnPBuf + kk * 32, 16, 1024);
-                                tc_mma_f16(tmem + kDnColO + 64 * m, ad, bd, kDnIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
-                            }
-                        tc_commit(smem_addr(&ms.v_free[p]));
-                    }
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        } else if (warp < kDnSoftmaxWarp) {
-            // ------------------------------- producers -------------------------------
-            if (nk > 0) {
-                const int e = tid & (kTile - 1), cp = tid >> 6;
-                const int32_t *bt = a.block_table + (size_t)pc.b * a.max_pages + pc.kv0;
-                const int left = pc.L - pc.kv0 * kPage;   // positions of the sequence from the piece's first page on
-                auto fetch = [&](PageEntry &en, int page, int t) {
-                    const bool page_ok = page >= 0 && page < a.num_pages;
-                    if (!page_ok && tid == 0) report(a.ws, CSA_ERR_DEVICE_DATA, pc.kv0 + t);
-                    en.fetch(a, page, page_ok && t * kPage + e < left, e, cp);
-                };
-                PageEntry raw0, raw1;   // tiles of even and of odd index
-                fetch(raw0, bt[0], 0);
-                if (nk > 1) fetch(raw1, bt[1], 1);
-                int page = nk > 2 ? bt[2] : 0;   // the page of the tile fetched next
-                load_q_rows(a, ms, pc, tmem);
-                uint32_t v[32];   // the next tile's row, dequantised before its buffer is free
-                raw0.dequant(v);
-                // rw holds tile t, already dequantised into v, so it takes tile t + 2 at once; rn holds t + 1
-                auto step = [&](int t, PageEntry &rw, const PageEntry &rn) {
-                    const uint32_t g = g0 + t, p = g % kDnStages;
-                    const unsigned int vb = __ballot_sync(0xffffffffu, rw.valid);
-                    const bool nan = rw.has_nan();
-                    if (t + 2 < nk) {
-                        fetch(rw, page, t + 2);
-                        if (t + 3 < nk) page = bt[t + 3];
-                    }
-                    if (g >= kDnStages) ok = ok && warp_wait(&ms.v_free[p], (g / kDnStages - 1u) & 1u, &ms.abort_flag, a.ws, 5);
-                    if (ok) {
-                        uint8_t *dst = V + p * kDnVBuf + cp * kDnVChunk;
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            *reinterpret_cast<uint4 *>(dst + swz((uint32_t)e, (uint32_t)u)) =
-                                make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-                        if (nan) {
-                            ms.nan_entry[p][e] = g + 1u;
-                            ms.nan_tile[p] = g + 1u;
-                        }
-                    }
-                    if (cp == 0 && lane == 0) reinterpret_cast<volatile uint32_t *>(&ms.vmask[p])[warp] = vb;
-                    fence_async_smem();
-                    warp_arrive(&ms.v_ready[p]);
-                    if (t + 1 < nk) rn.dequant(v);
-                };
-#pragma unroll 1
-                for (int t = 0; t < nk; t += 2) {
-                    step(t, raw0, raw1);
-                    if (t + 1 < nk) step(t + 1, raw1, raw0);
-                }
-            }
-        } else {
-            // ------------------------------- softmax -------------------------------
-            const int q = warp - kDnSoftmaxWarp;     // TMEM quarter: rows 16q .. 16q+15
-            const int u = lane >> 4;                 // this thread's entries 32u .. 32u+31 of a tile
-            const int hl = 16 * q + (lane & 15);     // this thread's row
-            const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
-            const uint32_t row = pc.r0 + (uint32_t)hl;
-            const int tok = (int)(row / (uint32_t)a.H), head = (int)(row % (uint32_t)a.H);
-            const int pos = pc.L - pc.n + tok;
-            int lo = 0, hi = 0;                      // positions the row sees
-            float slope = 0.f;                       // of the distance bias, log2 domain
-            if (hl < pc.rows) {
-                hi = pos + 1;
-                if (a.spans) {
-                    const int2 s = a.spans[pc.c0 + tok];
-                    lo = max(s.x, 0);
-                    hi = min(s.y, pc.L);
-                }
-                if (a.slopes) slope = a.slopes[head] * kLog2e;
-            }
-            float m_run = kNoMax;                    // the row's running maximum (log2 domain), as the partner has it
-            float lsum = 0.f;                        // this thread's share of the row's denominator
-            if (nk > 0) ok = bar_and(1, kDnSoftmax, ok && warp_wait(&ms.q_ready, pieces & 1u, &ms.abort_flag, a.ws, 11));
-            const float zs = ms.zs[hl];
-            for (int t = 0; t < nk; ++t) {
-                const uint32_t g = g0 + t, p = g % kDnStages, sb = g & 1u;
-                // v_ready: the producers' valid-entry mask of this tile; s_full: both halves of its scores
-                ok = bar_and(1, kDnSoftmax, ok && warp_wait(&ms.v_ready[p], (g / kDnStages) & 1u, &ms.abort_flag, a.ws, 9) &&
-                                                warp_wait(&ms.s_full[sb], (g >> 1) & 1u, &ms.abort_flag, a.ws, 6));
-                if (!ok) {
-                    warp_arrive(&ms.s_free[sb]);
-                    warp_arrive(&ms.p_full[p]);
-                    continue;
-                }
-                tc_fence_after();
-                // z[j] = S_0 + S_1 of entry 32u + j of row hl (unscaled)
-                float z[32];
-#pragma unroll
-                for (int pcs = 0; pcs < 2; ++pcs) {
-                    float s0[16], s1[16];
-                    tc_ld16x32bx2_x16_pair(tq + kDnColS + 64 * sb + 16 * pcs,
-                                           tq + (16u << 16) + kDnColS + 64 * sb + 16 * pcs, s0, s1);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z[16 * pcs + i] = s0[i] + s1[i];
-                }
-                tc_fence_before();
-                warp_arrive(&ms.s_free[sb]);   // QK of tile g + 2 may overwrite these columns
-                const int e0 = (pc.kv0 + t) * kPage + 32 * u;   // position of z[0]
-                float zf = zs;                                  // z -> log2 domain
-                if (a.softcap > 0.f) {
-                    // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap))): absolute error a few 2^-24 cap
-                    const float arg = 2.f * zs / a.softcap, cap = a.softcap * kLog2e;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = cap * (1.f - __fdividef(2.f, 1.f + exp2f(z[i] * arg)));
-                    zf = 1.f;
-                }
-                if (a.slopes) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = fmaf(z[i], zf, -slope * fabsf((float)(pos - e0 - i)));
-                    zf = 1.f;
-                }
-                if (ms.nan_tile[p] == g + 1u) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (ms.nan_entry[p][32 * u + i] == g + 1u) z[i] = __int_as_float(0x7FC00000);
-                }
-                // entries that are valid and that the row sees
-                uint32_t seen = (uint32_t)(ms.vmask[p] >> (32 * u));
-                if (lo > e0) seen &= lo - e0 < 32 ? 0xFFFFFFFFu << (lo - e0) : 0u;
-                if (hi < e0 + 32) seen &= hi > e0 ? 0xFFFFFFFFu >> (32 - (hi - e0)) : 0u;
-                if (seen != 0xFFFFFFFFu) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!((seen >> i) & 1u)) z[i] = -INFINITY;
-                }
-                float mt = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) mt = fmaxf(mt, z[i]);
-                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16)) * zf;   // zf > 0
-                const bool need = mt > m_run + kLazy;
-                if (bar_or(1, kDnSoftmax, need)) {
-                    // some row's maximum grew: new maxima, and O^T rescaled column by column
-                    const float mn = need ? fmaxf(m_run, mt) : m_run;
-                    const float al = exp2f(m_run - mn);   // 0 while m_run is kNoMax, 1 if unchanged
-                    if (u == 0) ms.alpha[hl] = al;
-                    lsum *= al;
-                    m_run = mn;
-                    bar_sync(1, kDnSoftmax);   // every row's factor visible
-                    if (t > 0) {
-                        // this warp's lanes of the four O^T M-tiles, once PV of the previous tile has completed
-                        const uint32_t gp = g - 1u;
-                        ok = warp_wait(&ms.v_free[gp % kDnStages], (gp / kDnStages) & 1u, &ms.abort_flag, a.ws, 7);
-                        if (ok) {
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int k = 0; k < 32; ++k) {
-                                float o[8];
-                                const uint32_t col = kDnColO + 8 * k;   // M-tile k/8, rows 8(k%8) ..
-                                tc_ld8_sync(tq + col, o);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) o[i] *= ms.alpha[8 * (k & 7) + i];
-                                tc_st8(tq + col, o);
-                            }
-                            tc_wait_st();
-                        }
-                    }
-                }
-                // P^T row hl, entries 32u .. 32u+31: four 16-byte units of the 128-byte swizzled row;
-                // p = 2^(z zf - m + 7), 0 for a masked entry (z = -inf)
-                const float mref = m_run - kPOffset;
-                float ls = 0.f;
-                uint8_t *Pb = P + p * kDnPBuf;
-#pragma unroll
-                for (int gq = 0; gq < 4; ++gq) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p0 = exp2f(fmaf(z[8 * gq + 2 * i], zf, -mref));
-                        const float p1 = exp2f(fmaf(z[8 * gq + 2 * i + 1], zf, -mref));
-                        ls += p0 + p1;
-                        pk[i] = pack_f16x2(p0, p1);
-                    }
-                    *reinterpret_cast<uint4 *>(Pb + swz((uint32_t)hl, (uint32_t)(4 * u + gq))) =
-                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
-                lsum += ls;
-                fence_async_smem();
-                tc_fence_before();
-                warp_arrive(&ms.p_full[p]);
-            }
-            lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);   // the row's two halves
-            if (u == 0 && hl < pc.rows) {
-                if (pc.first && pc.last) {
-                    // a row that sees nothing: out = 0, lse = -inf (a NaN sum stays NaN)
-                    ms.inv[hl] = lsum == 0.f ? 0.f : 1.f / lsum;
-                    a.lse[pc.row + hl] = lsum == 0.f ? -INFINITY : (m_run - kPOffset) * kLn2 + logf(lsum);
-                } else {
-                    const int slot = 2 * (int)blockIdx.x + (pc.first ? 1 : 0);
-                    a.part_ml[(size_t)slot * kDenseRows + hl] = make_float2(m_run - kPOffset, lsum);
-                }
-            }
-        }
-        // ---- epilogue: O^T, M-tile w/4, quarter w%4, by warps 0-15
         if (nk > 0) {
-            const uint32_t gl = g0 + nk - 1;
-            ok = ok && warp_wait(&ms.v_free[gl % kDnStages], (gl / kDnStages) & 1u, &ms.abort_flag, a.ws, 8);
-        }
-        ok = bar_and(4, kDnThreads, ok);
-        if (tid < kDenseRows) ms.qmax[tid] = 0u;
-        if (ok && warp < 16) {
+            if (warp == 0) dense_prefetch(ms.args, ms, &maps, V, pc, g0);
+            stage_q(a, ms, pc, x, V);
+            __syncthreads();
+            store_q(V, tmem);
+            tc_fence_before();
+            __syncthreads();
             tc_fence_after();
-            const int m = warp >> 2, qq = warp & 3, ch = 128 * m + 32 * qq + lane;
-            const bool whole = pc.first && pc.last;
-            float *po = a.part_o + ((size_t)(2 * blockIdx.x + (pc.first ? 1 : 0)) * kDenseRows) * kLatent + ch;
-            uint32_t *out = reinterpret_cast<uint32_t *>(a.out + (size_t)pc.row * kLatent + (ch & ~1));
-#pragma unroll
-            for (int hq = 0; hq < kDenseRows; hq += 16) {
-                float o[16];
-                if (nk > 0) {
-                    tc_ld16_sync(tmem + ((uint32_t)(32 * qq) << 16) + kDnColO + 64 * m + hq, o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-                }
-                if (!whole) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (hq + i < pc.rows) po[(size_t)(hq + i) * kLatent] = o[i];
-                } else {
-                    // lanes 2l and 2l + 1 exchange one row each, so that both store a channel pair
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float x0 = o[i] * ms.inv[hq + i], x1 = o[i + 1] * ms.inv[hq + i + 1];
-                        const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
-                        const int r = hq + i + (lane & 1);
-                        __nv_bfloat162 v = (lane & 1) ? __floats2bfloat162_rn(other, x1) : __floats2bfloat162_rn(x0, other);
-                        if (r < pc.rows) out[(size_t)r * (kLatent / 2)] = *reinterpret_cast<uint32_t *>(&v);
-                    }
-                }
-            }
         }
+
+        if (warp >= kDnCorrWarp) ok = dense_mma(pi, g0);
+        else if (warp < kDnProducerWarps) ok = nk == 0 || dense_produce(pi, g0, &maps);
+        else ok = dense_scores(pi, g0, sent);
+        ok = dense_epilogue(pi, g0, pieces, ok);
         if (nk > 0) {
             g0 += nk;
             ++pieces;
         }
     }
-    if (tid == 0) a.share[blockIdx.x] = ms.share;
-    if (warp >= kDnIssuerWarp && lane == 0) {
+    if (tid == 0 && x == 0) a.share[blockIdx.x >> 1] = ms.share;
+    // nothing is on its way to or from the other CTA when this one ends: what it sent here has been waited
+    // for tile by tile, and its last releases are waited for now
+    if (warp == kDnPvWarp && ok)
+        for (uint32_t i = 1; i <= (uint32_t)kDnPStages && i <= g0; ++i)
+            ok = ok && warp_wait_hint(&ms.p_free[(g0 - i) % kDnPStages], ((g0 - i) / kDnPStages) & 1u, cx, 18);
+    if (warp >= kDnScoreWarp && warp < kDnCorrWarp && ok && sent > 0)
+        warp_wait_hint(&ms.r_free[(warp - kDnScoreWarp) >> 2][warp & 3], (sent - 1u) & 1u, cx, 19);
+    if ((warp == kDnQkWarp || warp == kDnPvWarp) && lane == 0) {
         // every MMA this thread issued has completed before TMEM is released
-        tc_commit(smem_addr(&ms.final_bar[warp - kDnIssuerWarp]));
+        tc_commit(smem_addr(&ms.final_bar[warp - kDnQkWarp]));
         volatile int no_abort = 0;
-        mbar_wait(&ms.final_bar[warp - kDnIssuerWarp], 0, &no_abort, a.ws, 4);
+        mbar_wait(&ms.final_bar[warp - kDnQkWarp], 0, &no_abort, a.ws, 4);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kDnIssuerWarp) tc_dealloc(ms.tmem_base, kDnTmemCols);
+    if (warp == kDnQkWarp) tc_dealloc(ms.tmem_base, kDnTmemCols);
+    if (ms.abort_flag) {
+        // after a failed wait, stores to the other CTA may still be on their way
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 1000000ull) {}
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
 }
 
 // ------------------------------------------------------------------------------------------------
-// Combine: out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over the parts of a shared row tile, in CTA
-// order.  CTA (c, y) takes rows 8y .. 8y+7 of the row tile that CTA c of the attention began and did
-// not finish, one warp per row.
+// Combine: out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over the parts of a shared row tile, in
+// cluster order.  CTA (c, y) takes rows 8y .. 8y+7 of the row tile that cluster c began and did not
+// finish, one warp per row.
 // ------------------------------------------------------------------------------------------------
 constexpr int kCombineRows = 8;
 
 __global__ void __launch_bounds__(32 * kCombineRows) dense_combine_kernel(DenseArgs a)
 {
-    __shared__ int slots[kDenseCtas + 1];
+    __shared__ int slots[kDensePairs + 1];
     __shared__ int first_end, counts[kCombineRows];
-    __shared__ float wgt[kCombineRows][kDenseCtas + 1];
+    __shared__ float wgt[kCombineRows][kDensePairs + 1];
     grid_dep_wait();     // every part
     grid_dep_launch();   // a dependent kernel launched after this one waits for it before reading
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const DenseShare tail = a.share[c];
     const int r = kCombineRows * blockIdx.y + warp;
     if (tail.tail_rows <= kCombineRows * (int)blockIdx.y) return;
-    // the parts: the tail of CTA c, then the heads of the CTAs behind it up to the one that ends the tile
-    if (tid == 0) first_end = kDenseCtas;
+    // the parts: the tail of cluster c, then the heads of the clusters behind it up to the one that ends the tile
+    if (tid == 0) first_end = kDensePairs;
     __syncthreads();
     const int o = c + 1 + tid;
     DenseShare sh{};
-    if (o < kDenseCtas) sh = a.share[o];
+    if (o < kDensePairs) sh = a.share[o];
     if (sh.head && sh.head_ends) atomicMin(&first_end, o);
     __syncthreads();
     const bool part = sh.head && o <= first_end;
@@ -787,15 +1079,34 @@ __global__ void __launch_bounds__(32 * kCombineRows) dense_combine_kernel(DenseA
     if (lane == 0) a.lse[tail.tail_row + r] = den == 0.f ? -INFINITY : M * kLn2 + logf(den);
 }
 
+static cudaError_t cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t *pool, int num_pages, int bytes,
+                             CUtensorMapSwizzle swizzle, CUtensorMap *out)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)bytes, (cuuint64_t)kPage, (cuuint64_t)num_pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)bytes, (cuuint64_t)bytes * kPage};
+    const cuuint32_t box[3] = {(cuuint32_t)bytes / 2, (cuuint32_t)kPage, 1}, estr[3] = {1, 1, 1};
+    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(pool), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st)
 {
     static_assert(kDnSmem <= 232448, "shared memory budget");
-    static_assert(32 * kCombineRows >= kDenseCtas, "one thread per CTA behind the tail");
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(dense_attn_kernel), kDnSmem);
+    static_assert(32 * kCombineRows >= kDensePairs, "one thread per cluster behind the tail");
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    cudaError_t e = tensor_map_encoder(&encode);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(dense_attn_kernel, dim3(kDenseCtas), dim3(kDnThreads), kDnSmem, st, a);
+    DenseMaps maps;
+    if ((e = cache_map(encode, a.codes, a.num_pages, kCodeBytes, CU_TENSOR_MAP_SWIZZLE_128B, &maps.codes)) != cudaSuccess) return e;
+    if ((e = cache_map(encode, a.scales, a.num_pages, kScaleBytes, CU_TENSOR_MAP_SWIZZLE_NONE, &maps.scales)) != cudaSuccess) return e;
+    e = allow_dynamic_smem(reinterpret_cast<const void *>(dense_attn_kernel), kDnSmem);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(dense_combine_kernel, dim3(kDenseCtas, kDenseRows / kCombineRows), dim3(32 * kCombineRows), 0,
+    e = launch_overlapped(dense_attn_kernel, dim3(2 * kDensePairs), dim3(kDnThreads), kDnSmem, st, maps, a);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(dense_combine_kernel, dim3(kDensePairs, kDenseRows / kCombineRows), dim3(32 * kCombineRows), 0,
                              st, a);
 }
 

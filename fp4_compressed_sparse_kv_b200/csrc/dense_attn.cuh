@@ -5,15 +5,15 @@
 
 namespace csa {
 
-constexpr int kDenseRows = 64;           // query rows (token, head) of one row tile
-constexpr int kDenseCtas = kNumSms;      // one persistent CTA per SM
+constexpr int kDenseRows = 128;          // query rows (token, head) of one row tile
+constexpr int kDensePairs = kNumSms / 2; // persistent clusters of two CTAs, one CTA per SM
 
-// What a CTA left unfinished, for the combine: a row tile whose cache pages were shared with the next
-// CTA (tail: its first part, in partial slot 2c + 1) and one that an earlier CTA began (head: slot 2c).
+// What a cluster left unfinished, for the combine: a row tile whose cache pages were shared with the next
+// cluster (tail: its first part, in partial slot 2c + 1) and one that an earlier one began (head: slot 2c).
 struct DenseShare {
     long long tail_row;   // first row (token * H + head, over the whole call) of the tail's row tile
     int tail_rows;        // its rows, 0 for no tail
-    int head;             // 1: slot 2c holds a part of a row tile begun by an earlier CTA
+    int head;             // 1: slot 2c holds a part of a row tile begun by an earlier cluster
     int head_ends;        // 1: that part is the row tile's last
     int pad;
 };
@@ -37,9 +37,9 @@ struct DenseArgs {
     const int2 *spans;     // [rows] (lo, hi) or nullptr: causal
     uint16_t *out;
     float *lse;
-    DenseShare *share;     // [kDenseCtas]
-    float2 *part_ml;       // [2 kDenseCtas][kDenseRows] (running max, running sum)
-    float *part_o;         // [2 kDenseCtas][kDenseRows][512]
+    DenseShare *share;     // [kDensePairs]
+    float2 *part_ml;       // [2 kDensePairs][kDenseRows] (running max, running sum)
+    float *part_o;         // [2 kDensePairs][kDenseRows][512]
     void *ws;
 };
 
@@ -51,9 +51,9 @@ inline DenseWs dense_ws_layout()
 {
     DenseWs w;
     w.share = kHeaderBytes;
-    w.part_ml = align_up(w.share + kDenseCtas * sizeof(DenseShare), 256);
-    w.part_o = align_up(w.part_ml + (size_t)2 * kDenseCtas * kDenseRows * sizeof(float2), 256);
-    w.total = w.part_o + (size_t)2 * kDenseCtas * kDenseRows * kLatent * sizeof(float);
+    w.part_ml = align_up(w.share + kDensePairs * sizeof(DenseShare), 256);
+    w.part_o = align_up(w.part_ml + (size_t)2 * kDensePairs * kDenseRows * sizeof(float2), 256);
+    w.total = w.part_o + (size_t)2 * kDensePairs * kDenseRows * kLatent * sizeof(float);
     return w;
 }
 

@@ -45,6 +45,7 @@
 #include "convert.cuh"
 #include "pipeline.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.cuh"
 
 namespace csa {
 
@@ -215,15 +216,6 @@ struct ScrSmem {
 // kind::f8f6f4 instruction descriptor: D f32, A and B E4M3 (format 0), both K-major, M=128, N=32.
 constexpr uint32_t kIdescScreen =
     (1u << 4) | ((uint32_t)(kScrN >> 3) << 17) | ((uint32_t)(kScrRows >> 4) << 24);
-
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-            "r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
-}
 
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate)
@@ -507,26 +499,24 @@ __global__ void __launch_bounds__(kScrThreads, 1) screen_kernel(const __grid_con
 // ------------------------------------------------------------------------------------------------
 // Host side
 // ------------------------------------------------------------------------------------------------
-namespace {
-
-std::mutex g_encode_mu;
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-
-// The driver's tensor-map encoder, looked up once through the runtime (no link against libcuda).
 cudaError_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out)
 {
-    std::lock_guard<std::mutex> lock(g_encode_mu);
-    if (!g_encode) {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!encode) {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
         const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
         if (e != cudaSuccess) return e;
         if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    *out = g_encode;
+    *out = encode;
     return cudaSuccess;
 }
+
+namespace {
 
 // The keys' tensor map, re-encoded only when the key pool changes (the last one per device is kept).
 cudaError_t keys_tensor_map(const uint8_t *keys, int num_pages, CUtensorMap *out)

@@ -74,6 +74,15 @@ __device__ __forceinline__ void tc_commit(uint32_t mbar_saddr)
                  : "memory");
 }
 
+// The same on the mbarrier at this address in both CTAs of a cluster of two.
+__device__ __forceinline__ void tc_commit_both(uint32_t mbar_saddr)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(mbar_saddr),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
 __device__ __forceinline__ void tc_alloc(uint32_t dst_saddr, uint32_t ncols)
 {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_saddr), "r"(ncols)
