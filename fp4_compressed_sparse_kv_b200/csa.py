@@ -7,6 +7,7 @@ library is missing or a tensor is not on the GPU, these functions raise.
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -121,16 +122,15 @@ def lib():
     L.csa_kv_export.argtypes = [ctypes.POINTER(KVLayerC), P, i32, P, P, sz, P]
     L.csa_kv_import.restype = st
     L.csa_kv_import.argtypes = [ctypes.POINTER(KVLayerC), P, i32, P, P, sz, P]
+    # layer and batch: a structure's address or its bytes
     L.csa_kv_append_fp4.restype = st
-    L.csa_kv_append_fp4.argtypes = [ctypes.POINTER(KVLayerC), ctypes.POINTER(BatchC), P, i32, P, P, P, P, i32, P,
-                                    sz, P]
+    L.csa_kv_append_fp4.argtypes = [P, P, P, i32, P, P, P, P, i32, P, sz, P]
     L.csa_kv_unpack_fp4.restype = st
-    L.csa_kv_unpack_fp4.argtypes = [ctypes.POINTER(KVLayerC), ctypes.POINTER(BatchC), P, i32, P, P, sz, P]
+    L.csa_kv_unpack_fp4.argtypes = [P, P, P, i32, P, P, sz, P]
     L.csa_dense_attn_workspace_bytes.restype = sz
     L.csa_dense_attn_workspace_bytes.argtypes = []
     L.csa_dense_attn.restype = st
-    L.csa_dense_attn.argtypes = [ctypes.POINTER(KVLayerC), ctypes.POINTER(BatchC), P, i32, P, i32, ctypes.c_float,
-                                 ctypes.c_float, P, P, P, P, P, sz, P]
+    L.csa_dense_attn.argtypes = [P, P, P, i32, P, i32, ctypes.c_float, ctypes.c_float, P, P, P, P, P, sz, P]
     L.csa_check_device_error.restype = st
     L.csa_check_device_error.argtypes = [P, P, ctypes.POINTER(ctypes.c_int64)]
     L.csa_status_string.restype = ctypes.c_char_p
@@ -168,8 +168,10 @@ def _buf_ptr(t, name):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """Handle of `stream`, or of the current stream (without a Stream object, which costs 3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def default_sm_scale():
@@ -413,14 +415,50 @@ def kv_import(layer, block_table, n, src, ws, stream=None):
            "csa_kv_import")
 
 
-def _run_rows(batch, cu_rows, rows, **arrays):
-    """Rows of a ragged run: checks cu_rows and that every array has the dtype and shape given for it."""
-    if cu_rows.dtype != torch.int32 or cu_rows.numel() != batch.B + 1:
+# The calls over ragged runs are short enough that their arguments' marshalling counts: the layer and the
+# batch are packed as bytes laid out like KVLayerC and BatchC, which costs a third of a ctypes structure.
+_pack_layer = struct.Struct("=5Q2i").pack
+_pack_batch = struct.Struct("=i4xQQi4xQi4x").pack
+
+
+def _run_device(t, name):
+    """The current device, which has to be where the run's tensors are (`t` is one of them)."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        _ptr(t, name)
+        raise TypeError("%s must be a torch tensor" % name)
+    if dev != torch.cuda.current_device():
+        raise ValueError("%s is on device %d, which is not the current one" % (name, dev))
+    return dev
+
+
+def _run_ptr(t, name, dev):
+    """Address of a contiguous tensor on device dev; 0 for None."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+        _ptr(t, name)
+        raise ValueError("%s is not on the current device" % name)
+    return t.data_ptr()
+
+
+def _run_handles(layer, batch, dev):
+    """Bytes of the C structures of a layer and a batch."""
+    p = _run_ptr
+    return (_pack_layer(p(layer.codes, "codes", dev), p(layer.scales, "scales", dev), p(layer.keys, "keys", dev),
+                        p(layer.swa, "swa", dev), p(layer.swa_scale, "swa_scale", dev), layer.num_pages, layer.num_rows),
+            _pack_batch(batch.B, p(batch.seq_len, "seq_len", dev), p(batch.block_table, "block_table", dev),
+                        batch.max_pages, p(batch.swa_row, "swa_row", dev), batch.max_seq_len))
+
+
+def _run_rows(batch, cu_rows):
+    if cu_rows.dtype is not torch.int32 or cu_rows.numel() != batch.B + 1:
         raise ValueError("cu_rows must be int32 with batch.B + 1 entries")
-    for name, (t, dtype, shape) in arrays.items():
-        if t is not None and (t.dtype != dtype or tuple(t.shape) != shape):
-            raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
-    return int(rows)
+
+
+def _run_array(t, name, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError("%s must be %s of shape %s" % (name, dtype, list(shape)))
 
 
 def kv_append_fp4(layer, batch, cu_rows, latent, idx_key, ws, norm_weight=None, rope_table=None, stream=None):
@@ -428,25 +466,33 @@ def kv_append_fp4(layer, batch, cu_rows, latent, idx_key, ws, norm_weight=None, 
     (bf16 [rows, 512]) and idx_key (bf16 [rows, 128]) are the last positions of sequence b (batch.seq_len
     counts them).  norm_weight float32 [512] and rope_table float32 [positions, 32, 2] of (cos, sin) apply
     RMSNorm and the rotation of each row's position first; the last 128 positions also go to the window."""
-    rows = _run_rows(batch, cu_rows, latent.shape[0], latent=(latent, torch.bfloat16, (latent.shape[0], LATENT)),
-                     idx_key=(idx_key, torch.bfloat16, (latent.shape[0], IDX_DIM)),
-                     norm_weight=(norm_weight, torch.float32, (LATENT,)))
-    if rope_table is not None and (rope_table.dtype != torch.float32 or tuple(rope_table.shape[1:]) != (32, 2)):
-        raise ValueError("rope_table must be float32 of shape [positions, 32, 2]")
-    lc, bc = layer.c(), batch.c()
-    _check(lib().csa_kv_append_fp4(ctypes.byref(lc), ctypes.byref(bc), _ptr(cu_rows, "cu_rows"), rows,
-                                   _ptr(latent, "latent"), _ptr(idx_key, "idx_key"), _ptr(norm_weight, "norm_weight"),
-                                   _ptr(rope_table, "rope_table"), 0 if rope_table is None else rope_table.shape[0],
-                                   _ptr(ws, "ws"), ws.numel(), _stream(stream)), "csa_kv_append_fp4")
+    rows = latent.shape[0]
+    _run_rows(batch, cu_rows)
+    _run_array(latent, "latent", torch.bfloat16, (rows, LATENT))
+    _run_array(idx_key, "idx_key", torch.bfloat16, (rows, IDX_DIM))
+    if norm_weight is not None:
+        _run_array(norm_weight, "norm_weight", torch.float32, (LATENT,))
+    positions = 0
+    if rope_table is not None:
+        positions = rope_table.shape[0]
+        _run_array(rope_table, "rope_table", torch.float32, (positions, 32, 2))
+    dev, p = _run_device(ws, "ws"), _run_ptr
+    lc, bc = _run_handles(layer, batch, dev)
+    _check(lib().csa_kv_append_fp4(lc, bc, p(cu_rows, "cu_rows", dev), rows, p(latent, "latent", dev),
+                                   p(idx_key, "idx_key", dev), p(norm_weight, "norm_weight", dev),
+                                   p(rope_table, "rope_table", dev), positions, p(ws, "ws", dev), ws.numel(),
+                                   _stream(stream)), "csa_kv_append_fp4")
 
 
 def kv_unpack_fp4(layer, batch, cu_rows, latent, ws, stream=None):
     """Read a ragged run's FP4 entries back as values into latent, bf16 [rows, 512] (exact)."""
-    rows = _run_rows(batch, cu_rows, latent.shape[0], latent=(latent, torch.bfloat16, (latent.shape[0], LATENT)))
-    lc, bc = layer.c(), batch.c()
-    _check(lib().csa_kv_unpack_fp4(ctypes.byref(lc), ctypes.byref(bc), _ptr(cu_rows, "cu_rows"), rows,
-                                   _ptr(latent, "latent"), _ptr(ws, "ws"), ws.numel(), _stream(stream)),
-           "csa_kv_unpack_fp4")
+    rows = latent.shape[0]
+    _run_rows(batch, cu_rows)
+    _run_array(latent, "latent", torch.bfloat16, (rows, LATENT))
+    dev, p = _run_device(ws, "ws"), _run_ptr
+    lc, bc = _run_handles(layer, batch, dev)
+    _check(lib().csa_kv_unpack_fp4(lc, bc, p(cu_rows, "cu_rows", dev), rows, p(latent, "latent", dev), p(ws, "ws", dev),
+                                   ws.numel(), _stream(stream)), "csa_kv_unpack_fp4")
 
 
 def dense_attn_workspace(device="cuda", stream=None):
@@ -462,15 +508,21 @@ def dense_attn(layer, batch, cu_rows, q, out, lse, ws, sm_scale=None, softcap=0.
     the FP4 cache: out bf16 [rows, H, 512], lse float32 [rows, H].  Causal, or spans int32 [rows, 2] of the
     positions lo <= j < hi each row sees; softcap > 0 caps scores by softcap * tanh(s / softcap); slopes
     float32 [H] subtracts slopes[h] * |p - j|."""
-    R, H = int(q.shape[0]), int(q.shape[1])
-    rows = _run_rows(batch, cu_rows, R, q=(q, torch.bfloat16, (R, H, LATENT)), out=(out, torch.bfloat16, (R, H, LATENT)),
-                     lse=(lse, torch.float32, (R, H)), slopes=(slopes, torch.float32, (H,)),
-                     spans=(spans, torch.int32, (R, 2)))
-    lc, bc = layer.c(), batch.c()
-    _check(lib().csa_dense_attn(ctypes.byref(lc), ctypes.byref(bc), _ptr(cu_rows, "cu_rows"), rows, _ptr(q, "q"), H,
-                                float(default_sm_scale() if sm_scale is None else sm_scale), float(softcap),
-                                _ptr(slopes, "slopes"), _ptr(spans, "spans"), _ptr(out, "out"), _ptr(lse, "lse"),
-                                _ptr(ws, "ws"), ws.numel(), _stream(stream)), "csa_dense_attn")
+    rows, H = q.shape[0], q.shape[1]
+    _run_rows(batch, cu_rows)
+    _run_array(q, "q", torch.bfloat16, (rows, H, LATENT))
+    _run_array(out, "out", torch.bfloat16, (rows, H, LATENT))
+    _run_array(lse, "lse", torch.float32, (rows, H))
+    if slopes is not None:
+        _run_array(slopes, "slopes", torch.float32, (H,))
+    if spans is not None:
+        _run_array(spans, "spans", torch.int32, (rows, 2))
+    dev, p = _run_device(ws, "ws"), _run_ptr
+    lc, bc = _run_handles(layer, batch, dev)
+    _check(lib().csa_dense_attn(lc, bc, p(cu_rows, "cu_rows", dev), rows, p(q, "q", dev), H,
+                                default_sm_scale() if sm_scale is None else sm_scale, softcap,
+                                p(slopes, "slopes", dev), p(spans, "spans", dev), p(out, "out", dev), p(lse, "lse", dev),
+                                p(ws, "ws", dev), ws.numel(), _stream(stream)), "csa_dense_attn")
 
 
 def check_device_error(ws, stream=None):

@@ -6,6 +6,15 @@
 
 namespace csa {
 
+// True in one lane of a converged warp, always the same one.  The compiler then knows that one thread issues what
+// stands behind it: sixteen tcgen05.mma of 32 cycles each go out in 512 cycles (825 behind lane == 0).
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -98,21 +107,22 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
     return ok != 0;
 }
 
-// What a wait needs to give up: the CTA's abort flag and the workspace's status.
+// What a wait needs to give up: shared-memory addresses of the CTA's abort flag (int) and of the pointer to
+// the workspace.
 struct WaitCtx {
-    volatile int *abort_flag;
-    void *ws;
+    uint32_t abort_flag, ws;
 };
 
 // The rest of a wait that has not ended soon: as mbar_wait.
 __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, WaitCtx cx, int where)
 {
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(__cvta_shared_to_generic(cx.abort_flag));
     const unsigned long long t0 = global_ns();
     while (!mbar_try_wait_hint(bar, parity)) {
-        if (*cx.abort_flag) return false;
+        if (*abort_flag) return false;
         if (global_ns() - t0 > kWaitLimitNs) {
-            *cx.abort_flag = 1;
-            report(cx.ws, CSA_ERR_TIMEOUT, where);
+            *abort_flag = 1;
+            report(*reinterpret_cast<void **>(__cvta_shared_to_generic(cx.ws)), CSA_ERR_TIMEOUT, where);
             return false;
         }
     }
@@ -121,14 +131,15 @@ __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, WaitC
 
 // Wait of a whole warp, every lane in the same instructions (a wait of one lane whose outcome is then
 // broadcast leaves the warp split, and the code behind it runs once for each part: measured at half of all
-// instructions).  The outcome is the same in every lane.
+// instructions).  A phase that is already over costs one test (40 cycles; with a suspension time 70).
 __device__ __forceinline__ bool warp_wait_hint(uint64_t *bar, uint32_t parity, const WaitCtx &cx, int where)
 {
+    if (mbar_try_wait(bar, parity)) return true;
     const uint32_t b = smem_addr(bar);
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-        if (__all_sync(0xffffffffu, mbar_try_wait_hint(b, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait_long(b, parity, cx, where));
+        if (mbar_try_wait_hint(b, parity)) return true;
+    return mbar_wait_long(b, parity, cx, where);
 }
 
 }  // namespace csa

@@ -47,9 +47,10 @@ constexpr int kDnFlags = 8;                      // tiles whose page is known to
 constexpr int kDnGroups = 2;                     // tiles in their softmax at a time
 constexpr int kDnProducerWarps = 4;              // warps 0-3
 constexpr int kDnScoreWarp = 4;                  // warps 4-11: groups of four, one per TMEM quarter
-constexpr int kDnCorrWarp = kDnScoreWarp + 4 * kDnGroups;   // four warps, one per TMEM quarter
-constexpr int kDnQkWarp = kDnCorrWarp, kDnPvWarp = kDnCorrWarp + 1, kDnPlanWarp = kDnCorrWarp + 2;   // what else they do
-constexpr int kDnThreads = 32 * (kDnCorrWarp + 4);          // 128 registers each: a spill is a miss in the 20 KB of L1 left
+constexpr int kDnMmaWarp = kDnScoreWarp + 4 * kDnGroups;    // warps 12-15: PV, QK, next piece; each rescales a quarter of O
+constexpr int kDnPvWarp = kDnMmaWarp, kDnQkWarp = kDnMmaWarp + 1, kDnPlanWarp = kDnMmaWarp + 2;
+constexpr int kDnThreads = 32 * (kDnMmaWarp + 4);          // 128 registers each: a spill is a miss in the 20 KB of L1 left
+constexpr uint32_t kDnFailed = 0xFFFFFFFFu;
 constexpr uint32_t kDnVChunk = kTile * 128;              // 8 KB: 64 entries x 64 fp16
 constexpr uint32_t kDnVBuf = kDnCh / 64 * kDnVChunk;     // 32 KB per tile buffer
 constexpr uint32_t kDnPBuf = kDenseRows * 128;           // 16 KB: 128 rows x 64 entries fp16
@@ -65,7 +66,6 @@ constexpr uint32_t kDnTmemCols = 512;
 constexpr uint32_t kDnColO = 0;                  // O_x: 256 channels
 constexpr uint32_t kDnColQ = 256;                // Q_x: 256 channels, two per column
 constexpr uint32_t kDnColS = 384;                // S_x of tile g: columns 384 + 64(g%2) ..
-constexpr uint32_t kDnPBytes = kDenseRows / 2 * (128 + 4);   // of P and rescale factors, from the other CTA
 constexpr long long kDnMinTiles = 2;             // pages a cluster takes at least
 constexpr int kDnPieceCost = 8;                  // what a row tile costs besides its pages, in pages
 static_assert(kTile == kPage, "a tile is one page");
@@ -100,13 +100,17 @@ struct DenseMisc {
     uint64_t s_full[2], s_free[2];
     uint64_t r_full[kDnGroups][4];          // scores received, by softmax warp
     uint64_t r_free[kDnGroups][4];          // the other CTA has read those sent to it
-    uint64_t p_full[kDnPStages], p_free[kDnPStages], c_done[kDnPStages];
+    uint64_t p_full[kDnPStages], p_free[kDnPStages];
+    uint64_t go, c_done;                    // O is to be rescaled (or the piece is over); it has been
     uint64_t m_full[kDnGroups][4];          // rows' references after a tile, by softmax warp
     uint64_t inv_full;
     uint64_t final_bar[2];
     uint32_t nan_mask[kDnStages][kDnProducerWarps];    // entries with a NaN scale: bits of 32 entries per producer warp
+    uint4 flags[kDnStages];                            // entries with a NaN scale (two words), page valid
+    uint32_t go_slot;                                  // P buffer of the tile to rescale for, kDnFailed at the end
     int page_ok[kDnFlags];                             // the page id of tile g % 8 is valid
     uint32_t tmem_base;
+    uint32_t rescales;                                 // of O so far
     int abort_flag;
     long long warp_sum[kDnThreads / 32];
     DensePiece piece[2];
@@ -323,27 +327,24 @@ struct PageEntry {
         return valid && ((((sc.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sc.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u) != 0;
     }
 
-    // Channels 64h .. 64h + 63 as 32 fp16 pairs; zeros for an invalid or NaN entry.
-    __device__ __forceinline__ void dequant(int h, bool ok, uint32_t *v) const
+    // Channels 32c .. 32c + 31 as 16 fp16 pairs; zeros for an invalid or NaN entry.
+    __device__ __forceinline__ void dequant(int c, bool ok, uint32_t *v) const
     {
-        uint32_t sh[2];   // the four group scales as (s0, s1), (s2, s3)
-        e4m3x4_to_f16x2x2(h ? sc.y : sc.x, sh);
+        uint32_t sh[2];   // the four group scales of 64 channels as (s0, s1), (s2, s3)
+        e4m3x4_to_f16x2x2(c & 2 ? sc.y : sc.x, sh);
+        const uint32_t s01 = ok ? sh[c & 1] : 0u;
+        const uint4 cw = code[c];
 #pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-            const uint32_t s2 = __byte_perm(sh[gg >> 1], 0u, (gg & 1) ? 0x3232u : 0x1010u);
-            const uint4 cw = code[2 * h + (gg >> 1)];
+        for (int gg = 0; gg < 2; ++gg) {
+            const uint32_t s2 = __byte_perm(s01, 0u, gg ? 0x3232u : 0x1010u);
             uint32_t c0[4], c1[4];
-            e2m1x8_to_f16x2x4((gg & 1) ? cw.z : cw.x, c0);
-            e2m1x8_to_f16x2x4((gg & 1) ? cw.w : cw.y, c1);
+            e2m1x8_to_f16x2x4(gg ? cw.z : cw.x, c0);
+            e2m1x8_to_f16x2x4(gg ? cw.w : cw.y, c1);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 v[8 * gg + q] = hmul2_u32(c0[q], s2);
                 v[8 * gg + 4 + q] = hmul2_u32(c1[q], s2);
             }
-        }
-        if (!ok) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
         }
     }
 };
@@ -420,105 +421,170 @@ __device__ __forceinline__ uint8_t *dense_smem()
 
 __device__ __forceinline__ DenseMisc &dense_misc(uint8_t *base) { return *reinterpret_cast<DenseMisc *>(base + kDnOffMisc); }
 
+__device__ __forceinline__ WaitCtx dense_wait(DenseMisc &ms) { return WaitCtx{smem_addr(&ms.abort_flag), smem_addr(&ms.args.ws)}; }
+
 // ------------------------------------------------------------------------------------------------
 // Roles of the warps while a piece runs.  Each is a function of its own: the register allocation of one
 // does not see what the others keep, and nothing is spilled inside a tile loop (the L1 beside 200 KB of
 // shared memory holds no stack: a reload costs an L2 access).  They return false after a failed wait.
 // ------------------------------------------------------------------------------------------------
-// Rescaling of O, MMA issue, next piece.
-__device__ __noinline__ bool dense_mma(int pi, uint32_t g0)
+// This warp's quarter of O times the rescale factors of the tile in P buffer pp, PV of the tile before having completed.
+__device__ __forceinline__ void dense_rescale(DenseMisc &ms, uint32_t tmem, int q, uint32_t pp)
+{
+    const float al = ms.alpha[pp][32 * q + (threadIdx.x & 31)];
+    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kDnColO;
+    tc_fence_after();
+#pragma unroll 1
+    for (int k = 0; k < kDnCh; k += 32) {
+        float o[32];
+        tc_ld32_sync(to + k, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= al;
+        tc_st32(to + k, o);
+    }
+    tc_wait_st();
+    tc_fence_before();
+}
+
+// PV of every tile, once its P has come from both CTAs and O is at its scale; the commits release the tile's V buffer
+// and, in both CTAs, its P buffer.  When a row's maximum has grown, the four MMA warps rescale O first.
+__device__ __noinline__ bool dense_pv(int pi, uint32_t g0)
 {
     uint8_t *base = dense_smem();
     DenseMisc &ms = dense_misc(base);
-    const DenseArgs &a = ms.args;
     const DensePiece &pc = ms.piece[pi];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const WaitCtx cx{&ms.abort_flag, a.ws};
+    const int lane = threadIdx.x & 31, nk = pc.kv1 - pc.kv0, rows = pc.rows;
+    const WaitCtx cx = dense_wait(ms);
     const uint32_t tmem = ms.tmem_base;
-    const int nk = pc.kv1 - pc.kv0;
+    const uint64_t p_desc = umma_sdesc_sw128(smem_addr(base) + kDnOffP, 16, 1024);
+    const uint64_t v_desc = umma_sdesc_sw128(smem_addr(base), kDnVChunk, 1024);
+    uint32_t rescales = ms.rescales;
     bool ok = true;
-    uint8_t *V = base, *P = base + kDnOffP;
-    const int q = warp & 3;
-    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + kDnColO;
-    const uint32_t sV = smem_addr(V), sP = smem_addr(P);
-    // QK into S of tile g (columns of parity g % 2) once the producers have written the tile and the
-    // score warps have read tile g - 2's scores
-    auto issue_qk = [&](int t) {
-        const uint32_t g = g0 + t, p = g % kDnStages, sb = g & 1u;
-        if (!warp_wait_hint(&ms.v_ready[p], (g / kDnStages) & 1u, cx, 3)) return false;
-        if (g >= 2 && !warp_wait_hint(&ms.s_free[sb], ((g >> 1) - 1u) & 1u, cx, 10)) return false;
-        if (lane == 0) {
-            tc_fence_after();
-#pragma unroll 4
-            for (int k = 0; k < kDnCh / 16; ++k) {
-                const uint64_t bd = umma_sdesc_sw128(sV + p * kDnVBuf + (k >> 2) * kDnVChunk + (k & 3) * 32, 16, 1024);
-                tc_mma_f16_ts(tmem + kDnColS + 64 * sb, tmem + kDnColQ + 8 * k, bd, kDnIdescQK, k > 0 ? 1u : 0u);
-            }
-            tc_commit(smem_addr(&ms.s_full[sb]));
-        }
-        __syncwarp();
-        return true;
-    };
-    if (lane == 0 && warp == kDnPlanWarp) next_piece(a, ms.cur, ms.share, ms.piece[pi ^ 1]);
-    __syncwarp();
 #pragma unroll 1
-    for (int t = -2; ok && t < nk; ++t) {
-        if (warp == kDnQkWarp && t + 2 < nk) {
-            ok = issue_qk(t + 2);
-            if (!ok) break;
-        }
-        if (t < 0) continue;
+    for (int t = 0; t < nk; ++t) {
         const uint32_t g = g0 + t, p = g % kDnStages, pp = g % kDnPStages;
         ok = warp_wait_hint(&ms.p_full[pp], (g / kDnPStages) & 1u, cx, 7);
         if (!ok) break;
-        const float al = ms.alpha[pp][32 * q + lane];
-        if (t > 0 && 32 * q < pc.rows && __any_sync(0xffffffffu, al != 1.f)) {
-            // some row's maximum grew: this warp's rows of O, once PV of the previous tile has completed
-            const uint32_t gp = g - 1u;
-            ok = warp_wait_hint(&ms.v_free[gp % kDnStages], (gp / kDnStages) & 1u, cx, 13);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int k = 0; k < kDnCh; k += 32) {
-                float o[32];
-                tc_ld32_sync(tq + k, o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= al;
-                tc_st32(tq + k, o);
+        if (t > 0) {
+            const float4 al = reinterpret_cast<const float4 *>(ms.alpha[pp])[lane];   // rows 4 lane ..
+            const bool one = al.x == 1.f && al.y == 1.f && al.z == 1.f && al.w == 1.f;
+            if (__any_sync(0xffffffffu, !one && (4 * lane & ~31) < rows)) {
+                const uint32_t gp = g - 1u;
+                ok = warp_wait_hint(&ms.v_free[gp % kDnStages], (gp / kDnStages) & 1u, cx, 13);
+                if (!ok) break;
+                if (lane == 0) ms.go_slot = pp;
+                __syncwarp();
+                lane0_arrive(&ms.go, lane);
+                dense_rescale(ms, tmem, kDnPvWarp & 3, pp);
+                ok = warp_wait_hint(&ms.c_done, rescales & 1u, cx, 12);
+                if (!ok) break;
+                ++rescales;
             }
-            tc_wait_st();
-            tc_fence_before();
+        }
+        tc_fence_after();
+        // descriptor addresses count 16-byte units
+        const uint64_t ad = p_desc + pp * (kDnPBuf >> 4), bd = v_desc + p * (kDnVBuf >> 4);
+        if (elect_lane()) {
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+                tc_mma_f16(tmem + kDnColO, ad + 2 * kk, bd + 128 * kk, kDnIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
+            tc_commit_both(smem_addr(&ms.p_free[pp]));
+            tc_commit(smem_addr(&ms.v_free[p]));
         }
         __syncwarp();
-        lane0_arrive(&ms.c_done[pp], lane);
-        if (warp == kDnPvWarp) {
-            // PV once O is at its scale; the commits release the tile's V buffer and, in both CTAs, its
-            // P buffer
-            ok = warp_wait_hint(&ms.c_done[pp], (g / kDnPStages) & 1u, cx, 12);
-            if (!ok) break;
+    }
+    if (lane == 0) {
+        ms.go_slot = kDnFailed;   // the other MMA warps are done too
+        ms.rescales = rescales;
+    }
+    __syncwarp();
+    lane0_arrive(&ms.go, lane);
+    return ok;
+}
+
+// The other MMA warps: QK of every tile and the next piece, by one of them each, and rescaling of their quarter of O
+// when the PV warp asks.  n_go counts its requests.
+__device__ __noinline__ uint32_t dense_mma(int pi, uint32_t g0, uint32_t n_go)
+{
+    uint8_t *base = dense_smem();
+    DenseMisc &ms = dense_misc(base);
+    const DensePiece &pc = ms.piece[pi];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nk = pc.kv1 - pc.kv0;
+    const WaitCtx cx = dense_wait(ms);
+    const uint32_t tmem = ms.tmem_base;
+    const uint64_t v_desc = umma_sdesc_sw128(smem_addr(base), 16, 1024);
+    if (warp == kDnPlanWarp && lane == 0) next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
+    __syncwarp();
+    // a request of the PV warp: false at the end of the piece
+    auto serve = [&]() {
+        ++n_go;
+        const uint32_t pp = ms.go_slot;
+        if (pp == kDnFailed) return false;
+        dense_rescale(ms, tmem, warp & 3, pp);
+        __syncwarp();
+        lane0_arrive(&ms.c_done, lane);
+        return true;
+    };
+    if (warp == kDnQkWarp) {
+        // waits for a barrier and serves requests meanwhile; gives up after a long time, or when the piece is over
+        auto wait_serving = [&](uint64_t *bar, uint32_t parity) {
+            for (uint32_t i = 0; i < (1u << 22); ++i) {
+                if (mbar_test_wait(bar, parity)) return true;   // a try_wait would sleep through the request
+                if (mbar_test_wait(&ms.go, n_go & 1u) && !serve()) return false;
+                if ((i & 255u) == 255u && *(volatile int *)&ms.abort_flag) return false;
+            }
+            return mbar_wait_long(smem_addr(bar), parity, cx, 3);
+        };
+#pragma unroll 1
+        for (int t = 0; t < nk; ++t) {
+            const uint32_t g = g0 + t, p = g % kDnStages, sb = g & 1u;
+            // QK into S of tile g (columns of parity g % 2) once the producers have written the tile and the score warps
+            // have read tile g - 2's scores
+            if (!wait_serving(&ms.v_ready[p], (g / kDnStages) & 1u)) return kDnFailed;
+            if (g >= 2 && !wait_serving(&ms.s_free[sb], ((g >> 1) - 1u) & 1u)) return kDnFailed;
             if (lane == 0) {
-                tc_fence_after();
+                ms.flags[p] = make_uint4(ms.nan_mask[p][0] | ms.nan_mask[p][2], ms.nan_mask[p][1] | ms.nan_mask[p][3],
+                                         (uint32_t)ms.page_ok[g % kDnFlags], 0u);
+                mbar_arrive(&ms.s_full[sb]);   // the flags; the scores by the commit
+            }
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t bd = v_desc + p * (kDnVBuf >> 4);
+            const uint32_t sc = tmem + kDnColS + 64 * sb;
+            if (elect_lane()) {
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk) {
-                    const uint64_t ad = umma_sdesc_sw128(sP + pp * kDnPBuf + kk * 32, 16, 1024);
-                    const uint64_t bd = umma_sdesc_sw128(sV + p * kDnVBuf + kk * 2048, kDnVChunk, 1024);
-                    tc_mma_f16(tmem + kDnColO, ad, bd, kDnIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
-                }
-                tc_commit_both(smem_addr(&ms.p_free[pp]));
-                tc_commit(smem_addr(&ms.v_free[p]));
+                for (int k = 0; k < kDnCh / 16; ++k)
+                    tc_mma_f16_ts(sc, tmem + kDnColQ + 8 * k, bd + (k >> 2) * (kDnVChunk >> 4) + 2 * (k & 3), kDnIdescQK, k > 0 ? 1u : 0u);
+                tc_commit(smem_addr(&ms.s_full[sb]));
             }
             __syncwarp();
         }
     }
-    return ok;
+    for (;;) {
+        if (!warp_wait_hint(&ms.go, n_go & 1u, cx, 10)) return kDnFailed;
+        if (!serve()) return n_go;
+    }
 }
 
-// Page of tile t of a piece to shared memory, by warp 0; `ids` holds the page ids of tiles t & ~31 ..
+// The order of a piece's pages: with a distance bias from the last to the first, so that the newest positions set the
+// rows' references and O is hardly ever rescaled (23 rows of six sequences of 50,021 positions: 149 us, upwards 204);
+// otherwise upwards, so that the page that causal rows see in part comes last (2,048 rows behind 14,336 positions:
+// 4,514 us, downwards 4,595).
+struct PageOrder {
+    int first, step;
+    __device__ __forceinline__ PageOrder(const DenseArgs &a, const DensePiece &pc)
+        : first(a.slopes ? pc.kv1 - 1 : pc.kv0), step(a.slopes ? -1 : 1)
+    {
+    }
+    __device__ __forceinline__ int page(int t) const { return first + step * t; }
+};
+
+// Page of tile t to shared memory, by warp 0; `ids` holds the page ids of tiles t & ~31 ..
 __device__ __forceinline__ void dense_fetch(const DenseArgs &a, DenseMisc &ms, const DenseMaps *maps, uint8_t *base, int ids, int t,
-                                            uint32_t g, int kv0)
+                                            uint32_t g, int where)
 {
-    const int lane = threadIdx.x & 31, page = __shfl_sync(0xffffffffu, ids, t & 31);
-    if (lane == 0) {
+    const int page = __shfl_sync(0xffffffffu, ids, t & 31);
+    if (elect_lane()) {
         const uint32_t st = g % kDnRawStages;
         const bool ok = page >= 0 && page < a.num_pages;
         ms.page_ok[g % kDnFlags] = ok;
@@ -528,7 +594,7 @@ __device__ __forceinline__ void dense_fetch(const DenseArgs &a, DenseMisc &ms, c
             tma_load_3d(smem_addr(base + kDnOffC + st * kDnRawCodes), &maps->codes, 128 * x, 0, page, &ms.raw_full[st]);
             tma_load_3d(smem_addr(base + kDnOffSc + st * kDnRawScales), &maps->scales, 16 * x, 0, page, &ms.raw_full[st]);
         } else {
-            report(a.ws, CSA_ERR_DEVICE_DATA, kv0 + t);
+            report(a.ws, CSA_ERR_DEVICE_DATA, where);
             mbar_arrive(&ms.raw_full[st]);
         }
     }
@@ -540,8 +606,9 @@ __device__ __forceinline__ void dense_prefetch(const DenseArgs &a, DenseMisc &ms
                                                const DensePiece &pc, uint32_t g0)
 {
     const int nk = pc.kv1 - pc.kv0, lane = threadIdx.x & 31;
-    const int ids = lane < nk ? a.block_table[(size_t)pc.b * a.max_pages + pc.kv0 + lane] : -1;
-    for (int t = 0; t < min(nk, 2); ++t) dense_fetch(a, ms, maps, base, ids, t, g0 + t, pc.kv0);
+    const PageOrder po(a, pc);
+    const int ids = lane < nk ? a.block_table[(size_t)pc.b * a.max_pages + po.page(lane)] : -1;
+    for (int t = 0; t < min(nk, 2); ++t) dense_fetch(a, ms, maps, base, ids, t, g0 + t, po.page(t));
 }
 
 // Pages of the piece, dequantised, into the V buffers.
@@ -552,12 +619,12 @@ __device__ __noinline__ bool dense_produce(int pi, uint32_t g0, const DenseMaps 
     const DenseArgs &a = ms.args;
     const DensePiece &pc = ms.piece[pi];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const WaitCtx cx{&ms.abort_flag, a.ws};
-    const int nk = pc.kv1 - pc.kv0, kv0 = pc.kv0;
-    const int32_t *bt = a.block_table + (size_t)pc.b * a.max_pages + kv0;
-    const int left = pc.L - kv0 * kPage;   // positions of the sequence from the piece's first page on
+    const WaitCtx cx = dense_wait(ms);
+    const int nk = pc.kv1 - pc.kv0, L = pc.L;
+    const PageOrder po(a, pc);
+    const int32_t *bt = a.block_table + (size_t)pc.b * a.max_pages;
     const int e = tid & (kTile - 1), cp = tid >> 6;
-    int ids = lane < nk ? bt[lane] : -1, ids_next = 32 + lane < nk ? bt[32 + lane] : -1;
+    int ids = lane < nk ? bt[po.page(lane)] : -1, ids_next = 32 + lane < nk ? bt[po.page(32 + lane)] : -1;
     bool ok = true;
 #pragma unroll 1
     for (int t = 0; ok && t < nk; ++t) {
@@ -568,15 +635,15 @@ __device__ __noinline__ bool dense_produce(int pi, uint32_t g0, const DenseMaps 
             if (!ok) break;
             if (((t + 2) & 31) == 0) {
                 ids = ids_next;
-                ids_next = t + 34 + lane < nk ? bt[t + 34 + lane] : -1;
+                ids_next = t + 34 + lane < nk ? bt[po.page(t + 34 + lane)] : -1;
             }
-            dense_fetch(a, ms, maps, base, ids, t + 2, gf, kv0);
+            dense_fetch(a, ms, maps, base, ids, t + 2, gf, po.page(t + 2));
         }
         ok = warp_wait_hint(&ms.raw_full[st], (g / kDnRawStages) & 1u, cx, 21);
         if (!ok) break;
         PageEntry raw;
         raw.read(base + kDnOffC + st * kDnRawCodes, base + kDnOffSc + st * kDnRawScales, e, cp);
-        raw.valid = ms.page_ok[g % kDnFlags] && t * kPage + e < left;
+        raw.valid = ms.page_ok[g % kDnFlags] && po.page(t) * kPage + e < L;
         __syncwarp();
         lane0_arrive(&ms.raw_free[st], lane);
         const bool is_nan = raw.has_nan(), use = raw.valid && !is_nan;
@@ -585,12 +652,12 @@ __device__ __noinline__ bool dense_produce(int pi, uint32_t g0, const DenseMaps 
         if (!ok) break;
         uint8_t *dst = base + p * kDnVBuf + 2 * cp * kDnVChunk;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t v[32];
-            raw.dequant(h, use, v);
+        for (int c = 0; c < 4; ++c) {
+            uint32_t v[16];
+            raw.dequant(c, use, v);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4 *>(dst + h * kDnVChunk + swz((uint32_t)e, (uint32_t)u)) =
+            for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4 *>(dst + (c >> 1) * kDnVChunk + swz((uint32_t)e, (uint32_t)(4 * (c & 1) + u))) =
                     make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
         }
         if (lane == 0) ms.nan_mask[p][warp] = nan;
@@ -601,8 +668,11 @@ __device__ __noinline__ bool dense_produce(int pi, uint32_t g0, const DenseMaps 
     return ok;
 }
 
-// Scores and softmax.
-__device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
+// Scores and softmax.  Warp (group a, quarter q) takes the tiles g with g % kDnGroups == a.  In its TMEM quarter lanes
+// 16y .. 16y + 15 are rows of CTA y: it sends the other CTA's 16 rows of partial scores there and does the softmax of
+// its own 16, thread i < 16 entries 0-31 of row i, thread 16 + i entries 32-63.  n_sent counts the tiles whose scores
+// the warp has sent (and received).
+__device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_sent)
 {
     uint8_t *base = dense_smem();
     DenseMisc &ms = dense_misc(base);
@@ -610,24 +680,19 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
     const DensePiece &pc = ms.piece[pi];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int x = (int)cluster_rank();
-    const WaitCtx cx{&ms.abort_flag, a.ws};
-    const uint32_t tmem = ms.tmem_base;
+    const WaitCtx cx = dense_wait(ms);
+    const uint32_t tmem = ms.tmem_base, peer = (uint32_t)(x ^ 1);
     const int nk = pc.kv1 - pc.kv0;
-    bool ok = true;
-    uint8_t *P = base + kDnOffP, *R = base + kDnOffR;
-    const uint32_t peer = (uint32_t)(x ^ 1);
-    uint32_t sent = n_sent;
-    // Warp (group a, quarter q) takes the tiles g with g % kDnGroups == a.  In its TMEM quarter lanes 16y ..
-    // 16y + 15 are rows of CTA y: it sends the other CTA's 16 rows of partial scores there and does the softmax
-    // of its own 16, thread i < 16 entries 0-31 of row i, thread 16 + i entries 32-63.
-    const int q = warp & 3, grp = (warp - kDnScoreWarp) >> 2;
-    const int u = lane >> 4;
+    const PageOrder po(a, pc);
+    const int q = warp & 3, grp = (warp - kDnScoreWarp) >> 2, u = lane >> 4;
     const int hl = 32 * q + 16 * x + (lane & 15);   // this thread's TMEM lane and row of the row tile
     const int hr = 16 * q + (lane & 15);            // row among this CTA's
     const bool active = 32 * q < pc.rows;           // the quarter has rows (the same in both CTAs)
     const uint32_t ts = tmem + ((uint32_t)(32 * q + 16 * x) << 16) + kDnColS;
     const uint32_t to = tmem + ((uint32_t)(32 * q + 16 * (x ^ 1)) << 16) + kDnColS;
     const float zs = ms.zs[hl], zo = ms.zs[hl ^ 16];
+    const float softcap = a.softcap;
+    const bool biased = a.slopes != nullptr;
     const uint32_t row = pc.r0 + (uint32_t)hl;
     const int tok = (int)(row / (uint32_t)a.H);
     const int pos = pc.L - pc.n + tok;
@@ -640,23 +705,27 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
             lo = max(s.x, 0);
             hi = min(s.y, pc.L);
         }
-        if (a.slopes) slope = a.slopes[row - (uint32_t)tok * (uint32_t)a.H] * kLog2e;
+        if (biased) slope = a.slopes[row - (uint32_t)tok * (uint32_t)a.H] * kLog2e;
     }
-    const uint32_t pr = remote_addr(smem_addr(P), peer);
-    const uint32_t rr = remote_addr(smem_addr(R) + kDnRBuf * grp + 4096u * q + 16u * lane, peer);
-    const uint4 *rbuf = reinterpret_cast<const uint4 *>(R + kDnRBuf * grp + 4096 * q) + lane;
+    __syncwarp();
+    const uint32_t rbase = remote_addr(smem_addr(base), peer);   // of this CTA's shared memory in the other one
+    const uint32_t r_at = kDnOffR + kDnRBuf * grp + 4096u * q + 16u * lane;
+    const uint32_t r_full_there = remote_addr(smem_addr(&ms.r_full[grp][q]), peer);
+    const uint32_t r_free_there = remote_addr(smem_addr(&ms.r_free[grp][q]), peer);
+    uint32_t sent = n_sent;
+    bool ok = true;
     float m_run = kNoMax;                    // the reference of this thread's sum (log2 domain)
     float lsum = 0.f;                        // its share of the row's denominator
 #pragma unroll 1
     for (int t = (int)((uint32_t)(grp + kDnGroups - (int)(g0 % kDnGroups)) % kDnGroups); t < nk; t += kDnGroups) {
-        const uint32_t g = g0 + t, p = g % kDnStages, sb = g & 1u, pp = g % kDnPStages;
+        const uint32_t g = g0 + t, sb = g & 1u, pp = g % kDnPStages;
         if (active) lane0_arrive_expect_tx(&ms.r_full[grp][q], 4096u, lane);
-        ok = ok && warp_wait_hint(&ms.v_ready[p], (g / kDnStages) & 1u, cx, 9) &&
-             warp_wait_hint(&ms.s_full[sb], (g >> 1) & 1u, cx, 6);
+        ok = warp_wait_hint(&ms.s_full[sb], (g >> 1) & 1u, cx, 6);
         if (ok && active && sent > 0) ok = warp_wait_hint(&ms.r_free[grp][q], (sent - 1u) & 1u, cx, 14);
         if (!ok) break;
-        const uint32_t nan = ms.nan_mask[p][u] | ms.nan_mask[p][2 + u];   // entries with a NaN scale in this CTA's channels
-        const bool page_ok = ms.page_ok[g % kDnFlags];
+        const uint4 fl = ms.flags[g % kDnStages];
+        const uint32_t nan = u ? fl.y : fl.x;   // entries of this thread with a NaN scale in this CTA's channels
+        const bool page_ok = fl.z != 0u;
         float z[32];
         tc_fence_after();
         if (active) {
@@ -668,13 +737,12 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
                 for (int i = 0; i < 32; ++i)
                     if ((nan >> i) & 1u) z[i] = __int_as_float(0x7FC00000);
             }
-            const uint32_t rb = remote_addr(smem_addr(&ms.r_full[grp][q]), peer);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                st_async16(rr + 512u * i,
+                st_async16(rbase + r_at + 512u * i,
                            make_uint4(__float_as_uint(z[4 * i]), __float_as_uint(z[4 * i + 1]),
                                       __float_as_uint(z[4 * i + 2]), __float_as_uint(z[4 * i + 3])),
-                           rb);
+                           r_full_there);
             tc_ld16x32bx2_x32(ts + 64 * sb, z);
         }
         tc_fence_before();
@@ -683,27 +751,27 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
         float al = 1.f;
         if (active) {
             ok = warp_wait_hint(&ms.r_full[grp][q], sent & 1u, cx, 15);
-            ++sent;
             if (!ok) break;
+            ++sent;
             // z = both halves of the channels, log2 domain
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint4 o = rbuf[32 * i];
+                const uint4 o = *reinterpret_cast<const uint4 *>(base + r_at + 512 * i);
                 z[4 * i] = fmaf(z[4 * i], zs, __uint_as_float(o.x));
                 z[4 * i + 1] = fmaf(z[4 * i + 1], zs, __uint_as_float(o.y));
                 z[4 * i + 2] = fmaf(z[4 * i + 2], zs, __uint_as_float(o.z));
                 z[4 * i + 3] = fmaf(z[4 * i + 3], zs, __uint_as_float(o.w));
             }
             __syncwarp();
-            lane0_arrive_remote(remote_addr(smem_addr(&ms.r_free[grp][q]), peer), lane);
-            const int e0 = (pc.kv0 + t) * kPage + 32 * u;   // position of z[0]
-            if (a.softcap > 0.f) {
+            lane0_arrive_remote(r_free_there, lane);
+            const int e0 = po.page(t) * kPage + 32 * u;   // position of z[0]
+            if (softcap > 0.f) {
                 // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap))): absolute error a few 2^-24 cap
-                const float arg = 2.f / a.softcap, cap = a.softcap * kLog2e;
+                const float arg = 2.f / softcap, cap = softcap * kLog2e;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = cap * (1.f - __fdividef(2.f, 1.f + exp2f(z[i] * arg)));
             }
-            if (a.slopes) {
+            if (biased) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = fmaf(-slope, fabsf((float)(pos - e0 - i)), z[i]);
             }
@@ -712,11 +780,11 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
                 for (int i = 0; i < 32; ++i)
                     if ((nan >> i) & 1u) z[i] = __int_as_float(0x7FC00000);
             }
-            // entries of a mapped page that the row sees
-            uint32_t seen = page_ok ? 0xFFFFFFFFu : 0u;
-            if (lo > e0) seen &= lo - e0 < 32 ? 0xFFFFFFFFu << (lo - e0) : 0u;
-            if (hi < e0 + 32) seen &= hi > e0 ? 0xFFFFFFFFu >> (32 - (hi - e0)) : 0u;
-            if (seen != 0xFFFFFFFFu) {
+            if (lo > e0 || hi < e0 + 32 || !page_ok) {
+                // entries of a mapped page that the row sees
+                uint32_t seen = page_ok ? 0xFFFFFFFFu : 0u;
+                if (lo > e0) seen &= lo - e0 < 32 ? 0xFFFFFFFFu << (lo - e0) : 0u;
+                if (hi < e0 + 32) seen &= hi > e0 ? 0xFFFFFFFFu >> (32 - (hi - e0)) : 0u;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (!((seen >> i) & 1u)) z[i] = -INFINITY;
@@ -747,10 +815,9 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
         if (g >= kDnPStages) ok = warp_wait_hint(&ms.p_free[pp], (g / kDnPStages - 1u) & 1u, cx, 16);
         if (!ok) break;
         if (active) {
-            // P row hl, entries 32u .. 32u+31, here and in the other CTA: four 16-byte units of the
-            // 128-byte swizzled row; p = 2^(z - m + 7), 0 for a masked entry (z = -inf)
+            // P row hl, entries 32u .. 32u+31: four 16-byte units of the 128-byte swizzled row; p = 2^(z - m + 7), 0
+            // for a masked entry (z = -inf)
             const float mref = m_run - kPOffset;
-            const uint32_t pf = remote_addr(smem_addr(&ms.p_full[pp]), peer);
             float ls = 0.f;
 #pragma unroll
             for (int gq = 0; gq < 4; ++gq) {
@@ -762,27 +829,27 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
                     ls += p0 + p1;
                     pk[i] = pack_f16x2(p0, p1);
                 }
-                const uint4 w = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                const uint32_t at = pp * kDnPBuf + swz((uint32_t)hl, (uint32_t)(4 * u + gq));
-                *reinterpret_cast<uint4 *>(P + at) = w;
+                *reinterpret_cast<uint4 *>(base + kDnOffP + pp * kDnPBuf + swz((uint32_t)hl, (uint32_t)(4 * u + gq))) =
+                    make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
             if (u == 0) ms.alpha[pp][hl] = al;
             lsum += ls;
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                // the 16 rows are contiguous: one copy of 2 KB (16-byte stores to 16 rows cost twice the time and
-                // slow every other access of the shared memory)
-                const uint32_t r16 = 32u * q + 16u * x;
-                bulk_to_cta(pr + pp * kDnPBuf + 128u * r16, smem_addr(P) + pp * kDnPBuf + 128u * r16, 2048u, pf);
-                bulk_to_cta(remote_addr(smem_addr(&ms.alpha[pp][r16]), peer), smem_addr(&ms.alpha[pp][r16]), 64u, pf);
+            if (elect_lane()) {
+                // to the other CTA: the 16 rows are contiguous, one copy of 2 KB (16-byte stores to 16 rows cost twice
+                // the time and slow every other access of the shared memory)
+                const uint32_t r16 = 32u * q + 16u * x, pf = remote_addr(smem_addr(&ms.p_full[pp]), peer);
+                const uint32_t src = kDnOffP + pp * kDnPBuf + 128u * r16, asrc = smem_addr(&ms.alpha[pp][r16]);
+                bulk_to_cta(rbase + src, smem_addr(base) + src, 2048u, pf);
+                bulk_to_cta(remote_addr(asrc, peer), asrc, 64u, pf);
             }
         }
         __syncwarp();
-        if (active) lane0_arrive_expect_tx(&ms.p_full[pp], kDnPBytes / 4, lane);
+        if (active) lane0_arrive_expect_tx(&ms.p_full[pp], 2048u + 64u, lane);
         else lane0_arrive(&ms.p_full[pp], lane);
     }
-    // the row's denominator from its two threads of every group
+    // the row's denominator from its two threads in every group
     lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
     if (u == 0) ms.ml[grp][hr] = make_float2(m_run, lsum);
     bar_sync(1 + q, 32 * kDnGroups);
@@ -801,17 +868,16 @@ __device__ __noinline__ bool dense_scores(int pi, uint32_t g0, uint32_t &n_sent)
                 else
                     a.part_ml[(size_t)(2 * (blockIdx.x >> 1) + (pc.first ? 1 : 0)) * kDenseRows + hl] = make_float2(M - kPOffset, l);
             }
-            if (nk > 0 && ok) {
+            if (ok) {
                 ms.inv[hl] = inv;
                 st_async4(remote_addr(smem_addr(&ms.inv[hl]), peer), __float_as_uint(inv),
                           remote_addr(smem_addr(&ms.inv_full), peer));
             }
         }
         __syncwarp();
-        if (nk > 0) lane0_arrive_expect_tx(&ms.inv_full, 64u, lane);
+        lane0_arrive_expect_tx(&ms.inv_full, 64u, lane);
     }
-    n_sent = sent;
-    return ok;
+    return ok ? sent : kDnFailed;
 }
 
 // O of the piece to out or to a partial: quarter w%4, channels 64(w/4) .. of this CTA's, each warp through 4 KB
@@ -824,7 +890,7 @@ __device__ __noinline__ bool dense_epilogue(int pi, uint32_t g0, uint32_t pieces
     const DensePiece &pc = ms.piece[pi];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int x = (int)cluster_rank();
-    const WaitCtx cx{&ms.abort_flag, a.ws};
+    const WaitCtx cx = dense_wait(ms);
     const uint32_t tmem = ms.tmem_base;
     const int nk = pc.kv1 - pc.kv0;
     uint8_t *V = base;
@@ -834,7 +900,8 @@ __device__ __noinline__ bool dense_epilogue(int pi, uint32_t g0, uint32_t pieces
              warp_wait_hint(&ms.inv_full, pieces & 1u, cx, 17);
     }
     // the V buffers are free once every warp that reads or writes them has come here
-    if (__syncthreads_and(ok)) {
+    ok = __syncthreads_and(ok);
+    if (ok) {
         tc_fence_after();
         const int q = warp & 3, c0 = 64 * (warp >> 2), r0 = 32 * q;
         const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + kDnColO + c0;
@@ -909,7 +976,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
             mbar_init(&ms.v_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ms.s_full[i], 1);
+            mbar_init(&ms.s_full[i], 2);
             mbar_init(&ms.s_free[i], 4);
         }
         for (int i = 0; i < kDnGroups; ++i)
@@ -920,17 +987,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
         for (int i = 0; i < kDnPStages; ++i) {
             mbar_init(&ms.p_full[i], 4);
             mbar_init(&ms.p_free[i], 2);
-            mbar_init(&ms.c_done[i], 4);
         }
         for (int i = 0; i < kDnGroups; ++i)
             for (int w = 0; w < 4; ++w) mbar_init(&ms.m_full[i][w], 1);
+        mbar_init(&ms.go, 1);
+        mbar_init(&ms.c_done, 3);
         mbar_init(&ms.inv_full, 4);
         for (int r = 0; r < 2; ++r) mbar_init(&ms.final_bar[r], 1);
         ms.abort_flag = 0;
+        ms.rescales = 0;
         ms.args = a;
         fence_mbar_init();
     }
-    if (warp == kDnQkWarp) {
+    if (warp == kDnMmaWarp) {
         tc_alloc(smem_addr(&ms.tmem_base), kDnTmemCols);
         tc_relinquish();
     }
@@ -940,11 +1009,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
     cluster_arrive();
     cluster_wait();      // the other CTA's barriers are there, and it has read its plan from where P goes
 
-    const WaitCtx cx{&ms.abort_flag, a.ws};
+    const WaitCtx cx = dense_wait(ms);
     bool ok = true;
     uint32_t g0 = 0;      // tiles of the earlier pieces
     uint32_t pieces = 0;  // earlier pieces that had tiles
-    uint32_t sent = 0;    // score warps: tiles whose scores went to the other CTA (and came from there)
+    uint32_t sent = 0;    // score warps: tiles whose scores went to the other CTA (and came from there); MMA warps: requests
     for (int pi = 0;; pi ^= 1) {
         // the piece is visible and the previous one is finished with TMEM and shared memory
         tc_fence_before();
@@ -964,9 +1033,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
             tc_fence_after();
         }
 
-        if (warp >= kDnCorrWarp) ok = dense_mma(pi, g0);
-        else if (warp < kDnProducerWarps) ok = nk == 0 || dense_produce(pi, g0, &maps);
-        else ok = dense_scores(pi, g0, sent);
+        if (nk > 0) {
+            if (warp < kDnProducerWarps) ok = dense_produce(pi, g0, &maps);
+            else if (warp < kDnMmaWarp) sent = dense_scores(pi, g0, sent), ok = sent != kDnFailed;
+            else if (warp == kDnPvWarp) ok = dense_pv(pi, g0);
+            else sent = dense_mma(pi, g0, sent), ok = sent != kDnFailed;
+        } else if (warp == kDnPlanWarp && lane == 0) {
+            next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
+        } else if (warp == kDnScoreWarp && pc.first && pc.last) {
+            // no row of the tile sees anything
+            for (int i = lane; i < pc.rows; i += 32)
+                if (x == 0) ms.args.lse[pc.row + i] = -INFINITY;
+        }
         ok = dense_epilogue(pi, g0, pieces, ok);
         if (nk > 0) {
             g0 += nk;
@@ -979,18 +1057,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
     if (warp == kDnPvWarp && ok)
         for (uint32_t i = 1; i <= (uint32_t)kDnPStages && i <= g0; ++i)
             ok = ok && warp_wait_hint(&ms.p_free[(g0 - i) % kDnPStages], ((g0 - i) / kDnPStages) & 1u, cx, 18);
-    if (warp >= kDnScoreWarp && warp < kDnCorrWarp && ok && sent > 0)
+    if (warp >= kDnScoreWarp && warp < kDnMmaWarp && ok && sent > 0)
         warp_wait_hint(&ms.r_free[(warp - kDnScoreWarp) >> 2][warp & 3], (sent - 1u) & 1u, cx, 19);
-    if ((warp == kDnQkWarp || warp == kDnPvWarp) && lane == 0) {
+    if ((warp == kDnQkWarp || warp == kDnPvWarp) && elect_lane()) {
         // every MMA this thread issued has completed before TMEM is released
-        tc_commit(smem_addr(&ms.final_bar[warp - kDnQkWarp]));
+        uint64_t *done = &ms.final_bar[warp == kDnQkWarp ? 0 : 1];
+        tc_commit(smem_addr(done));
         volatile int no_abort = 0;
-        mbar_wait(&ms.final_bar[warp - kDnQkWarp], 0, &no_abort, a.ws, 4);
+        mbar_wait(done, 0, &no_abort, a.ws, 4);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kDnQkWarp) tc_dealloc(ms.tmem_base, kDnTmemCols);
+    if (warp == kDnMmaWarp) tc_dealloc(ms.tmem_base, kDnTmemCols);
     if (ms.abort_flag) {
         // after a failed wait, stores to the other CTA may still be on their way
         const unsigned long long t0 = global_ns();

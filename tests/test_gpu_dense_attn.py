@@ -162,6 +162,32 @@ def test_maximum_jumps_in_late_tiles():
     assert_close(attend(layer, r, q), reference(layer, r, q, None, 0.0, None))
 
 
+@pytest.mark.parametrize("biased", [False, True])
+def test_maximum_grows_page_by_page(biased):
+    """Every page outweighs those before it, whichever end the pages are taken from (a bias reverses their order): O is
+    rescaled at each page."""
+    r = Run([1, 3], [1500, 700], 43)
+    layer = random_layer(r.num_pages, 44)
+    q = queries(4, 64, 45)
+    slopes = torch.full((64,), 1e-3, device="cuda") if biased else None
+    at = 0
+    for b, n in enumerate(r.n):
+        v = values64(layer, r.slots(b, np.arange(r.lens[b])))
+        top = v[3 if biased else -5]
+        # entries grow along the way the pages are taken: scales double every other page, codes stay
+        pages = (r.lens[b] + 63) // 64
+        for k in range(pages):
+            step = k if not biased else pages - 1 - k
+            page = int(r.bt[b, k])
+            layer.scales[page] = 0x08 + 8 * min(8, step // 2) + (step % 2) * 4
+        v = values64(layer, r.slots(b, np.arange(r.lens[b])))
+        q[at:at + n] = (4 * torch.sign(top)[None, None] * torch.rand((n, 64, 1), device="cuda")).bfloat16()
+        at += n
+    got = attend(layer, r, q, slopes=slopes)
+    assert csa.check_device_error(got[2])[0] == 0
+    assert_close(got, reference(layer, r, q, None, 0.0, slopes))
+
+
 def test_scales_of_queries_in_one_tile():
     """Rows 80 binades apart share a row tile; zero rows give the plain average."""
     r = Run([4], [300], 17)
