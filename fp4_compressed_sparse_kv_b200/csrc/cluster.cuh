@@ -88,8 +88,8 @@ __device__ __forceinline__ void lane0_arrive_remote(uint32_t rbar, int lane)
 }
 
 // Waits of kernels whose warps run many different loops.  The code of all of them together has to fit the
-// SM's instruction cache, so a wait is a few instructions, with the hardware's suspension instead of polling,
-// and what bounds it stands out of line.  Remote stores and arrivals are waited for like local ones: what
+// SM's instruction cache, so a wait is a few instructions, with the hardware's suspension instead of polling, and no
+// call, around which the compiler would spill.  Remote stores and arrivals are waited for like local ones: what
 // they bring lies in this SM's shared memory when the barrier completes.  (Release and acquire at cluster
 // scope would also order global memory: a fence of some thousand cycles and an invalidated L1 per tile.)
 constexpr uint32_t kWaitHintNs = 4000;   // longest suspension of one try_wait
@@ -107,39 +107,35 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
     return ok != 0;
 }
 
-// What a wait needs to give up: shared-memory addresses of the CTA's abort flag (int) and of the pointer to
-// the workspace.
-struct WaitCtx {
-    uint32_t abort_flag, ws;
-};
-
-// The rest of a wait that has not ended soon: as mbar_wait.
-__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, WaitCtx cx, int where)
+__device__ __forceinline__ uint32_t global_ns_lo()
 {
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(__cvta_shared_to_generic(cx.abort_flag));
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait_hint(bar, parity)) {
-        if (*abort_flag) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            report(*reinterpret_cast<void **>(__cvta_shared_to_generic(cx.ws)), CSA_ERR_TIMEOUT, where);
-            return false;
-        }
-    }
-    return true;
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
 }
+
+// Shared-memory address of the CTA's abort flag (int): 0, or which wait ran past kWaitLimitNs.
+struct WaitCtx {
+    uint32_t abort_flag;
+};
 
 // Wait of a whole warp, every lane in the same instructions (a wait of one lane whose outcome is then
 // broadcast leaves the warp split, and the code behind it runs once for each part: measured at half of all
-// instructions).  A phase that is already over costs one test (40 cycles; with a suspension time 70).
+// instructions).  A phase that is already over costs one test (40 cycles; with a suspension time 70).  False, with the
+// abort flag set to `where`, when the wait runs past kWaitLimitNs, or when another warp's has.
 __device__ __forceinline__ bool warp_wait_hint(uint64_t *bar, uint32_t parity, const WaitCtx &cx, int where)
 {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint32_t b = smem_addr(bar);
+    const uint32_t b = smem_addr(bar), t0 = global_ns_lo();
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
+    do {
         if (mbar_try_wait_hint(b, parity)) return true;
-    return mbar_wait_long(b, parity, cx, where);
+        int aborted;
+        asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(aborted) : "r"(cx.abort_flag) : "memory");
+        if (aborted) return false;
+    } while (global_ns_lo() - t0 < (uint32_t)kWaitLimitNs);
+    asm volatile("st.volatile.shared.s32 [%0], %1;" ::"r"(cx.abort_flag), "r"(where) : "memory");
+    return false;
 }
 
 }  // namespace csa

@@ -66,7 +66,7 @@ constexpr uint32_t kDnTmemCols = 512;
 constexpr uint32_t kDnColO = 0;                  // O_x: 256 channels
 constexpr uint32_t kDnColQ = 256;                // Q_x: 256 channels, two per column
 constexpr uint32_t kDnColS = 384;                // S_x of tile g: columns 384 + 64(g%2) ..
-constexpr long long kDnMinTiles = 2;             // pages a cluster takes at least
+constexpr long long kDnMinTiles = 4;             // pages a cluster takes at least (one row tile of 64 pages: 27.5 us; 2: 30.7)
 constexpr int kDnPieceCost = 8;                  // what a row tile costs besides its pages, in pages
 static_assert(kTile == kPage, "a tile is one page");
 static_assert(kDnStages * kDnVBuf >= kDenseRows * kDnCh * 2, "Q is staged in the V buffers");
@@ -101,6 +101,7 @@ struct DenseMisc {
     uint64_t r_full[kDnGroups][4];          // scores received, by softmax warp
     uint64_t r_free[kDnGroups][4];          // the other CTA has read those sent to it
     uint64_t p_full[kDnPStages], p_free[kDnPStages];
+    uint64_t planned;                       // the next piece is known
     uint64_t go, c_done;                    // O is to be rescaled (or the piece is over); it has been
     uint64_t m_full[kDnGroups][4];          // rows' references after a tile, by softmax warp
     uint64_t inv_full;
@@ -136,6 +137,8 @@ __device__ __forceinline__ uint4 ld_stream16(const void *p)
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ------------------------------------------------------------------------------------------------
 // Work division.  Sequence b's row tiles have the numbers tile_base(b) .. tile_base(b + 1) - 1: at least
@@ -375,12 +378,12 @@ __device__ __forceinline__ void stage_q(const DenseArgs &a, DenseMisc &ms, const
             k = 13 - ((int)(top >> 23) - 127);
             k = k < -120 ? -120 : (k > 120 ? 120 : k);
         }
-        const float sc = exp2f((float)k);
+        const float sc = __int_as_float((127 + k) << 23);
         uint32_t h[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) h[m] = pack_f16x2(bf16_lo(ww[m]) * sc, bf16_hi(ww[m]) * sc);
         *reinterpret_cast<uint4 *>(stage + i * 512 + ((lane ^ (i & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (lane == 0) ms.zs[i] = a.sm_scale * exp2f((float)-k) * kLog2e;
+        if (lane == 0) ms.zs[i] = a.sm_scale * __int_as_float((127 - k) << 23) * kLog2e;
     }
 }
 
@@ -406,6 +409,13 @@ __device__ __forceinline__ void store_q(const uint8_t *stage, uint32_t tmem)
     tc_wait_st();
 }
 
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -421,7 +431,7 @@ __device__ __forceinline__ uint8_t *dense_smem()
 
 __device__ __forceinline__ DenseMisc &dense_misc(uint8_t *base) { return *reinterpret_cast<DenseMisc *>(base + kDnOffMisc); }
 
-__device__ __forceinline__ WaitCtx dense_wait(DenseMisc &ms) { return WaitCtx{smem_addr(&ms.abort_flag), smem_addr(&ms.args.ws)}; }
+__device__ __forceinline__ WaitCtx dense_wait(DenseMisc &ms) { return WaitCtx{smem_addr(&ms.abort_flag)}; }
 
 // ------------------------------------------------------------------------------------------------
 // Roles of the warps while a piece runs.  Each is a function of its own: the register allocation of one
@@ -513,7 +523,15 @@ __device__ __noinline__ uint32_t dense_mma(int pi, uint32_t g0, uint32_t n_go)
     const WaitCtx cx = dense_wait(ms);
     const uint32_t tmem = ms.tmem_base;
     const uint64_t v_desc = umma_sdesc_sw128(smem_addr(base), 16, 1024);
-    if (warp == kDnPlanWarp && lane == 0) next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
+    if (warp == kDnPlanWarp) {
+        if (lane == 0) next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
+        __syncwarp();
+        lane0_arrive(&ms.planned, lane);
+        // its Q rows to the L2: this CTA's half of each is four lines
+        const DensePiece &nx = ms.piece[pi ^ 1];
+        const uint16_t *src = ms.args.q + (size_t)nx.row * kLatent + kDnCh * (int)cluster_rank() + 64 * (lane & 3);
+        for (int r = lane >> 2; r < nx.rows; r += 8) prefetch_l2(src + (size_t)r * kLatent);
+    }
     __syncwarp();
     // a request of the PV warp: false at the end of the piece
     auto serve = [&]() {
@@ -526,14 +544,18 @@ __device__ __noinline__ uint32_t dense_mma(int pi, uint32_t g0, uint32_t n_go)
         return true;
     };
     if (warp == kDnQkWarp) {
-        // waits for a barrier and serves requests meanwhile; gives up after a long time, or when the piece is over
+        // waits for a barrier and serves requests meanwhile (testing: a try_wait would sleep through them)
         auto wait_serving = [&](uint64_t *bar, uint32_t parity) {
-            for (uint32_t i = 0; i < (1u << 22); ++i) {
-                if (mbar_test_wait(bar, parity)) return true;   // a try_wait would sleep through the request
+            if (mbar_test_wait(bar, parity)) return true;
+            const uint32_t t0 = global_ns_lo();
+#pragma unroll 1
+            do {
+                if (mbar_test_wait(bar, parity)) return true;
                 if (mbar_test_wait(&ms.go, n_go & 1u) && !serve()) return false;
-                if ((i & 255u) == 255u && *(volatile int *)&ms.abort_flag) return false;
-            }
-            return mbar_wait_long(smem_addr(bar), parity, cx, 3);
+                if (*(volatile int *)&ms.abort_flag) return false;
+            } while (global_ns_lo() - t0 < (uint32_t)kWaitLimitNs);
+            ms.abort_flag = 3;
+            return false;
         };
 #pragma unroll 1
         for (int t = 0; t < nk; ++t) {
@@ -602,17 +624,23 @@ __device__ __forceinline__ void dense_fetch(const DenseArgs &a, DenseMisc &ms, c
 }
 
 // The first two pages of a piece, ahead of everything else (warp 0).
-__device__ __forceinline__ void dense_prefetch(const DenseArgs &a, DenseMisc &ms, const DenseMaps *maps, uint8_t *base,
+__device__ __forceinline__ bool dense_prefetch(const DenseArgs &a, DenseMisc &ms, const DenseMaps *maps, uint8_t *base,
                                                const DensePiece &pc, uint32_t g0)
 {
     const int nk = pc.kv1 - pc.kv0, lane = threadIdx.x & 31;
     const PageOrder po(a, pc);
-    const int ids = lane < nk ? a.block_table[(size_t)pc.b * a.max_pages + po.page(lane)] : -1;
-    for (int t = 0; t < min(nk, 2); ++t) dense_fetch(a, ms, maps, base, ids, t, g0 + t, po.page(t));
+    const WaitCtx cx = dense_wait(ms);
+    const int ids = lane < min(nk, 2) ? a.block_table[(size_t)pc.b * a.max_pages + po.page(lane)] : -1;
+    for (int t = 0; t < min(nk, 2); ++t) {
+        const uint32_t g = g0 + t;
+        if (g >= kDnRawStages && !warp_wait_hint(&ms.raw_free[g % kDnRawStages], (g / kDnRawStages - 1u) & 1u, cx, 23)) return false;
+        dense_fetch(a, ms, maps, base, ids, t, g, po.page(t));
+    }
+    return true;
 }
 
 // Pages of the piece, dequantised, into the V buffers.
-__device__ __noinline__ bool dense_produce(int pi, uint32_t g0, const DenseMaps *maps)
+__device__ __noinline__ bool dense_produce(int pi, uint32_t g0, uint32_t n_planned, const DenseMaps *maps)
 {
     uint8_t *base = dense_smem();
     DenseMisc &ms = dense_misc(base);
@@ -664,6 +692,11 @@ __device__ __noinline__ bool dense_produce(int pi, uint32_t g0, const DenseMaps 
         fence_async_smem();
         __syncwarp();
         lane0_arrive(&ms.v_ready[p], lane);
+    }
+    if (warp == 0 && ok) {
+        // the next piece's first pages, while this one's last tiles go through the softmax
+        ok = warp_wait_hint(&ms.planned, n_planned & 1u, cx, 22);
+        if (ok && ms.piece[pi ^ 1].rows > 0) ok = dense_prefetch(a, ms, maps, base, ms.piece[pi ^ 1], g0 + nk);
     }
     return ok;
 }
@@ -766,14 +799,15 @@ __device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_se
             lane0_arrive_remote(r_free_there, lane);
             const int e0 = po.page(t) * kPage + 32 * u;   // position of z[0]
             if (softcap > 0.f) {
-                // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap))): absolute error a few 2^-24 cap
+                // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap))): absolute error a few 2^-23 cap
                 const float arg = 2.f / softcap, cap = softcap * kLog2e;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = cap * (1.f - __fdividef(2.f, 1.f + exp2f(z[i] * arg)));
+                for (int i = 0; i < 32; ++i) z[i] = fmaf(-2.f * cap, rcp(1.f + ex2(z[i] * arg)), cap);
             }
             if (biased) {
+                const float d = (float)(pos - e0);   // distances are whole numbers below 2^24, exact
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = fmaf(-slope, fabsf((float)(pos - e0 - i)), z[i]);
+                for (int i = 0; i < 32; ++i) z[i] = fmaf(-slope, fabsf(d - (float)i), z[i]);
             }
             if (nan) {
 #pragma unroll
@@ -880,6 +914,33 @@ __device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_se
     return ok ? sent : kDnFailed;
 }
 
+// A row tile no row of which sees anything (a whole one): lse, and the next piece.
+__device__ __noinline__ void dense_nothing_seen(int pi)
+{
+    DenseMisc &ms = dense_misc(dense_smem());
+    const DensePiece &pc = ms.piece[pi];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == kDnPlanWarp && lane == 0) next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
+    if (warp == kDnScoreWarp && cluster_rank() == 0)
+        for (int i = lane; i < pc.rows; i += 32) ms.args.lse[pc.row + i] = -INFINITY;
+}
+
+// The piece's Q into TMEM, and its first pages on their way unless they are already.
+__device__ __noinline__ void dense_begin(int pi, uint32_t g0, bool fetch, const DenseMaps *maps)
+{
+    uint8_t *base = dense_smem();
+    DenseMisc &ms = dense_misc(base);
+    const DensePiece &pc = ms.piece[pi];
+    const int warp = threadIdx.x >> 5;
+    if (warp == 0 && fetch) dense_prefetch(ms.args, ms, maps, base, pc, g0);   // a failure shows in the role
+    stage_q(ms.args, ms, pc, (int)cluster_rank(), base);
+    __syncthreads();
+    store_q(base, ms.tmem_base);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+}
+
 // O of the piece to out or to a partial: quarter w%4, channels 64(w/4) .. of this CTA's, each warp through 4 KB
 // of the V buffers so that its stores are whole rows of 128 bytes.
 __device__ __noinline__ bool dense_epilogue(int pi, uint32_t g0, uint32_t pieces, bool ok)
@@ -957,16 +1018,51 @@ __device__ __noinline__ bool dense_epilogue(int pi, uint32_t g0, uint32_t pieces
     return ok;
 }
 
+// The end of a CTA's work: its share for the combine, and nothing left on its way.
+__device__ __noinline__ void dense_finish(uint32_t g0, uint32_t sent, bool ok)
+{
+    DenseMisc &ms = dense_misc(dense_smem());
+    const int tid = threadIdx.x, warp = tid >> 5, x = (int)cluster_rank();
+    const WaitCtx cx = dense_wait(ms);
+    if (tid == 0 && x == 0) ms.args.share[blockIdx.x >> 1] = ms.share;
+    // nothing is on its way to or from the other CTA when this one ends: what it sent here has been waited
+    // for tile by tile, and its last releases are waited for now
+    if (warp == kDnPvWarp && ok)
+        for (uint32_t i = 1; i <= (uint32_t)kDnPStages && i <= g0; ++i)
+            ok = ok && warp_wait_hint(&ms.p_free[(g0 - i) % kDnPStages], ((g0 - i) / kDnPStages) & 1u, cx, 18);
+    if (warp >= kDnScoreWarp && warp < kDnMmaWarp && ok && sent > 0)
+        warp_wait_hint(&ms.r_free[(warp - kDnScoreWarp) >> 2][warp & 3], (sent - 1u) & 1u, cx, 19);
+    if ((warp == kDnQkWarp || warp == kDnPvWarp) && elect_lane()) {
+        // every MMA this thread issued has completed before TMEM is released
+        uint64_t *done = &ms.final_bar[warp == kDnQkWarp ? 0 : 1];
+        tc_commit(smem_addr(done));
+        volatile int no_abort = 0;
+        mbar_wait(done, 0, &no_abort, ms.args.ws, 4);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kDnMmaWarp) tc_dealloc(ms.tmem_base, kDnTmemCols);
+    if (ms.abort_flag) {
+        if (tid == 0) report(ms.args.ws, CSA_ERR_TIMEOUT, ms.abort_flag);
+        // after a failed wait, stores to the other CTA may still be on their way
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 1000000ull) {}
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
     dense_attn_kernel(const __grid_constant__ DenseMaps maps, DenseArgs a)
 {
     uint8_t *V = dense_smem();
     DenseMisc &ms = dense_misc(V);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int x = (int)cluster_rank();
+    const int warp = threadIdx.x >> 5;
     grid_dep_launch();   // the combine may be scheduled as CTAs finish
 
-    if (tid == 0) {
+    if (threadIdx.x == 0) {
         for (int i = 0; i < kDnRawStages; ++i) {
             mbar_init(&ms.raw_full[i], 1);
             mbar_init(&ms.raw_free[i], kDnProducerWarps);
@@ -990,6 +1086,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
         }
         for (int i = 0; i < kDnGroups; ++i)
             for (int w = 0; w < 4; ++w) mbar_init(&ms.m_full[i][w], 1);
+        mbar_init(&ms.planned, 1);
         mbar_init(&ms.go, 1);
         mbar_init(&ms.c_done, 3);
         mbar_init(&ms.inv_full, 4);
@@ -1009,41 +1106,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
     cluster_arrive();
     cluster_wait();      // the other CTA's barriers are there, and it has read its plan from where P goes
 
-    const WaitCtx cx = dense_wait(ms);
     bool ok = true;
     uint32_t g0 = 0;      // tiles of the earlier pieces
     uint32_t pieces = 0;  // earlier pieces that had tiles
+    bool prefetched = false;   // this piece's first pages are on their way: the producers of the one before saw to it
     uint32_t sent = 0;    // score warps: tiles whose scores went to the other CTA (and came from there); MMA warps: requests
     for (int pi = 0;; pi ^= 1) {
         // the piece is visible and the previous one is finished with TMEM and shared memory
         tc_fence_before();
         if (__syncthreads_or(!ok)) break;
         tc_fence_after();
-        const DensePiece &pc = ms.piece[pi];
-        if (pc.rows == 0) break;
-        const uint32_t tmem = ms.tmem_base;
-        const int nk = pc.kv1 - pc.kv0;
+        if (ms.piece[pi].rows == 0) break;
+        const int nk = ms.piece[pi].kv1 - ms.piece[pi].kv0;
+        if (nk > 0) dense_begin(pi, g0, !prefetched, &maps);
+        prefetched = nk > 0;
         if (nk > 0) {
-            if (warp == 0) dense_prefetch(ms.args, ms, &maps, V, pc, g0);
-            stage_q(a, ms, pc, x, V);
-            __syncthreads();
-            store_q(V, tmem);
-            tc_fence_before();
-            __syncthreads();
-            tc_fence_after();
-        }
-
-        if (nk > 0) {
-            if (warp < kDnProducerWarps) ok = dense_produce(pi, g0, &maps);
+            if (warp < kDnProducerWarps) ok = dense_produce(pi, g0, pieces, &maps);
             else if (warp < kDnMmaWarp) sent = dense_scores(pi, g0, sent), ok = sent != kDnFailed;
             else if (warp == kDnPvWarp) ok = dense_pv(pi, g0);
             else sent = dense_mma(pi, g0, sent), ok = sent != kDnFailed;
-        } else if (warp == kDnPlanWarp && lane == 0) {
-            next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
-        } else if (warp == kDnScoreWarp && pc.first && pc.last) {
-            // no row of the tile sees anything
-            for (int i = lane; i < pc.rows; i += 32)
-                if (x == 0) ms.args.lse[pc.row + i] = -INFINITY;
+        } else {
+            dense_nothing_seen(pi);
         }
         ok = dense_epilogue(pi, g0, pieces, ok);
         if (nk > 0) {
@@ -1051,33 +1134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
             ++pieces;
         }
     }
-    if (tid == 0 && x == 0) a.share[blockIdx.x >> 1] = ms.share;
-    // nothing is on its way to or from the other CTA when this one ends: what it sent here has been waited
-    // for tile by tile, and its last releases are waited for now
-    if (warp == kDnPvWarp && ok)
-        for (uint32_t i = 1; i <= (uint32_t)kDnPStages && i <= g0; ++i)
-            ok = ok && warp_wait_hint(&ms.p_free[(g0 - i) % kDnPStages], ((g0 - i) / kDnPStages) & 1u, cx, 18);
-    if (warp >= kDnScoreWarp && warp < kDnMmaWarp && ok && sent > 0)
-        warp_wait_hint(&ms.r_free[(warp - kDnScoreWarp) >> 2][warp & 3], (sent - 1u) & 1u, cx, 19);
-    if ((warp == kDnQkWarp || warp == kDnPvWarp) && elect_lane()) {
-        // every MMA this thread issued has completed before TMEM is released
-        uint64_t *done = &ms.final_bar[warp == kDnQkWarp ? 0 : 1];
-        tc_commit(smem_addr(done));
-        volatile int no_abort = 0;
-        mbar_wait(done, 0, &no_abort, a.ws, 4);
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == kDnMmaWarp) tc_dealloc(ms.tmem_base, kDnTmemCols);
-    if (ms.abort_flag) {
-        // after a failed wait, stores to the other CTA may still be on their way
-        const unsigned long long t0 = global_ns();
-        while (global_ns() - t0 < 1000000ull) {}
-    }
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
+    dense_finish(g0, sent, ok);
 }
 
 // ------------------------------------------------------------------------------------------------
