@@ -179,16 +179,17 @@ __device__ __forceinline__ int tile_weight(const DenseArgs &a, int c0, int n, in
 }
 
 // The next piece of the cluster's share, and what the share leaves unfinished.
-__device__ void next_piece(const DenseArgs &a, DenseCursor &cu, DenseShare &share, DensePiece &pc)
+__device__ void next_piece(const DenseArgs &a, const int32_t *cu_rows, const int32_t *seq_len, DenseCursor &cu, DenseShare &share,
+                           DensePiece &pc)
 {
     pc.rows = 0;
     while (cu.left > 0) {
-        const int c0 = a.cu_rows[cu.b], c1 = a.cu_rows[cu.b + 1], n = c1 - c0;
+        const int c0 = cu_rows[cu.b], c1 = cu_rows[cu.b + 1], n = c1 - c0;
         if (cu.tile >= tile_base(c1, cu.b + 1, a.H)) {
             if (++cu.b >= a.B) return;
             continue;
         }
-        int L = a.seq_len[cu.b];
+        int L = seq_len[cu.b];
         if (L > a.max_seq_len) L = 0;
         const uint32_t r0 = (uint32_t)(cu.tile - tile_base(c0, cu.b, a.H)) * kDenseRows;
         const int w = tile_weight(a, c0, n, L, r0);
@@ -281,17 +282,21 @@ __device__ void plan(const DenseArgs &a, DenseMisc &ms, int32_t *scratch)
     }
     if (lane == 31) ms.warp_sum[warp] = incl;
     __syncthreads();
-    long long before = 0, total = 0;
-    for (int i = 0; i < kDnThreads / 32; ++i) {
-        if (i < warp) before += ms.warp_sum[i];
-        total += ms.warp_sum[i];
+    long long sums = lane < kDnThreads / 32 ? ms.warp_sum[lane] : 0;   // inclusive, over the warps
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, sums, d);
+        if (lane >= d) sums += o;
     }
-    const long long excl = before + incl - sum;
+    const long long total = __shfl_sync(0xffffffffu, sums, 31);
+    const long long excl = (warp > 0 ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0) + incl - sum;
     // as many clusters as leave each kDnMinTiles pages
     const long long pairs = max(1ll, min((long long)gridDim.x / 2, total / kDnMinTiles));
     const int pair = blockIdx.x >> 1;
     if (pair < pairs) {
-        const long long s = total * pair / pairs, e = total * (pair + 1) / pairs;
+        // shares of total / pairs, the first total % pairs of them one longer
+        const long long each = total / pairs, more = total - each * pairs;
+        const long long s = each * pair + min((long long)pair, more), e = s + each + (pair < more ? 1 : 0);
         if (s < e && excl <= s && s < excl + sum) {
             long long at = excl;
             b = b0;
@@ -303,7 +308,7 @@ __device__ void plan(const DenseArgs &a, DenseMisc &ms, int32_t *scratch)
                 }
                 at += w;
             }
-            next_piece(a, ms.cur, ms.share, ms.piece[0]);
+            next_piece(a, s_cu, s_len, ms.cur, ms.share, ms.piece[0]);
         }
     }
 }
@@ -355,7 +360,8 @@ struct PageEntry {
 // This CTA's channels of the row tile's Q into `stage`, each row scaled by the power of two 2^k that puts its
 // largest |q| of these channels in [2^13, 2^14), 16-byte units swizzled; ms.zs gets tau * log2(e) * 2^-k.
 // Warp w: the rows of lanes 8w .. 8w+7 (a row per load, 512 contiguous bytes); zeros past the row tile's rows.
-__device__ __forceinline__ void stage_q(const DenseArgs &a, DenseMisc &ms, const DensePiece &pc, int x, uint8_t *stage)
+template <typename F>
+__device__ __forceinline__ void stage_q(const DenseArgs &a, DenseMisc &ms, const DensePiece &pc, int x, uint8_t *stage, F between)
 {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint4 qw[8];
@@ -365,6 +371,7 @@ __device__ __forceinline__ void stage_q(const DenseArgs &a, DenseMisc &ms, const
         qw[j] = make_uint4(0u, 0u, 0u, 0u);
         if (r < pc.rows) qw[j] = ld_stream16(a.q + (size_t)(pc.row + r) * kLatent + kDnCh * x + 8 * lane);
     }
+    between();   // the rows are on their way
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int i = 8 * w + j;
@@ -524,7 +531,7 @@ __device__ __noinline__ uint32_t dense_mma(int pi, uint32_t g0, uint32_t n_go)
     const uint32_t tmem = ms.tmem_base;
     const uint64_t v_desc = umma_sdesc_sw128(smem_addr(base), 16, 1024);
     if (warp == kDnPlanWarp) {
-        if (lane == 0) next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
+        if (lane == 0) next_piece(ms.args, ms.args.cu_rows, ms.args.seq_len, ms.cur, ms.share, ms.piece[pi ^ 1]);
         __syncwarp();
         lane0_arrive(&ms.planned, lane);
         // its Q rows to the L2: this CTA's half of each is four lines
@@ -920,7 +927,7 @@ __device__ __noinline__ void dense_nothing_seen(int pi)
     DenseMisc &ms = dense_misc(dense_smem());
     const DensePiece &pc = ms.piece[pi];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == kDnPlanWarp && lane == 0) next_piece(ms.args, ms.cur, ms.share, ms.piece[pi ^ 1]);
+    if (warp == kDnPlanWarp && lane == 0) next_piece(ms.args, ms.args.cu_rows, ms.args.seq_len, ms.cur, ms.share, ms.piece[pi ^ 1]);
     if (warp == kDnScoreWarp && cluster_rank() == 0)
         for (int i = lane; i < pc.rows; i += 32) ms.args.lse[pc.row + i] = -INFINITY;
 }
@@ -932,8 +939,9 @@ __device__ __noinline__ void dense_begin(int pi, uint32_t g0, bool fetch, const 
     DenseMisc &ms = dense_misc(base);
     const DensePiece &pc = ms.piece[pi];
     const int warp = threadIdx.x >> 5;
-    if (warp == 0 && fetch) dense_prefetch(ms.args, ms, maps, base, pc, g0);   // a failure shows in the role
-    stage_q(ms.args, ms, pc, (int)cluster_rank(), base);
+    stage_q(ms.args, ms, pc, (int)cluster_rank(), base, [&]() {
+        if (warp == 0 && fetch) dense_prefetch(ms.args, ms, maps, base, pc, g0);   // a failure shows in the role
+    });
     __syncthreads();
     store_q(base, ms.tmem_base);
     tc_fence_before();
@@ -1032,8 +1040,8 @@ __device__ __noinline__ void dense_finish(uint32_t g0, uint32_t sent, bool ok)
             ok = ok && warp_wait_hint(&ms.p_free[(g0 - i) % kDnPStages], ((g0 - i) / kDnPStages) & 1u, cx, 18);
     if (warp >= kDnScoreWarp && warp < kDnMmaWarp && ok && sent > 0)
         warp_wait_hint(&ms.r_free[(warp - kDnScoreWarp) >> 2][warp & 3], (sent - 1u) & 1u, cx, 19);
-    if ((warp == kDnQkWarp || warp == kDnPvWarp) && elect_lane()) {
-        // every MMA this thread issued has completed before TMEM is released
+    if (ms.abort_flag && (warp == kDnQkWarp || warp == kDnPvWarp) && elect_lane()) {
+        // every MMA this thread issued has completed before TMEM is released (otherwise the pieces' ends saw to it)
         uint64_t *done = &ms.final_bar[warp == kDnQkWarp ? 0 : 1];
         tc_commit(smem_addr(done));
         volatile int no_abort = 0;
@@ -1140,27 +1148,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kDnThreads, 1)
 // ------------------------------------------------------------------------------------------------
 // Combine: out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over the parts of a shared row tile, in
 // cluster order.  CTA (c, y) takes rows 8y .. 8y+7 of the row tile that cluster c began and did not
-// finish, one warp per row.
+// finish, two warps per row.
 // ------------------------------------------------------------------------------------------------
 constexpr int kCombineRows = 8;
 
-__global__ void __launch_bounds__(32 * kCombineRows) dense_combine_kernel(DenseArgs a)
+__global__ void __launch_bounds__(64 * kCombineRows) dense_combine_kernel(DenseArgs a)
 {
+    constexpr int kWarps = 2 * kCombineRows;
     __shared__ int slots[kDensePairs + 1];
-    __shared__ int first_end, counts[kCombineRows];
-    __shared__ float wgt[kCombineRows][kDensePairs + 1];
+    __shared__ int first_end, counts[kWarps];
+    __shared__ float wgt[kWarps][kDensePairs + 1];
+    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) first_end = kDensePairs;
     grid_dep_wait();     // every part
     grid_dep_launch();   // a dependent kernel launched after this one waits for it before reading
-    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const DenseShare tail = a.share[c];
-    const int r = kCombineRows * blockIdx.y + warp;
-    if (tail.tail_rows <= kCombineRows * (int)blockIdx.y) return;
-    // the parts: the tail of cluster c, then the heads of the clusters behind it up to the one that ends the tile
-    if (tid == 0) first_end = kDensePairs;
-    __syncthreads();
     const int o = c + 1 + tid;
     DenseShare sh{};
     if (o < kDensePairs) sh = a.share[o];
+    if (tail.tail_rows <= kCombineRows * (int)blockIdx.y) return;
+    // the parts: the tail of cluster c, then the heads of the clusters behind it up to the one that ends the tile
+    __syncthreads();
     if (sh.head && sh.head_ends) atomicMin(&first_end, o);
     __syncthreads();
     const bool part = sh.head && o <= first_end;
@@ -1168,13 +1176,14 @@ __global__ void __launch_bounds__(32 * kCombineRows) dense_combine_kernel(DenseA
     if (lane == 0) counts[warp] = __popc(vote);
     __syncthreads();
     int at = 1, n = 1;
-    for (int w = 0; w < kCombineRows; ++w) {
+    for (int w = 0; w < (kDensePairs + 31) / 32; ++w) {
         if (w < warp) at += counts[w];
         n += counts[w];
     }
     if (tid == 0) slots[0] = 2 * c + 1;
     if (part) slots[at + __popc(vote & ((1u << lane) - 1u))] = 2 * o;
     __syncthreads();
+    const int r = kCombineRows * blockIdx.y + (warp >> 1), half = warp & 1;
     if (r >= tail.tail_rows) return;
     float M = -INFINITY;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[(size_t)slots[i] * kDenseRows + r].x);
@@ -1190,13 +1199,13 @@ __global__ void __launch_bounds__(32 * kCombineRows) dense_combine_kernel(DenseA
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) den += __shfl_xor_sync(0xffffffffu, den, d);
     __syncwarp();
-    float4 acc[4] = {};
-#pragma unroll 4
+    float4 acc[2] = {};
+#pragma unroll 8
     for (int i = 0; i < n; ++i) {
-        const float4 *po = reinterpret_cast<const float4 *>(a.part_o + ((size_t)slots[i] * kDenseRows + r) * kLatent) + lane;
+        const float4 *po = reinterpret_cast<const float4 *>(a.part_o + ((size_t)slots[i] * kDenseRows + r) * kLatent) + 64 * half + lane;
         const float w = wgt[warp][i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2; ++j) {
             const float4 v = po[32 * j];
             acc[j].x = fmaf(w, v.x, acc[j].x);
             acc[j].y = fmaf(w, v.y, acc[j].y);
@@ -1205,14 +1214,14 @@ __global__ void __launch_bounds__(32 * kCombineRows) dense_combine_kernel(DenseA
         }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint2 *out = reinterpret_cast<uint2 *>(a.out + (size_t)(tail.tail_row + r) * kLatent) + lane;
+    uint2 *out = reinterpret_cast<uint2 *>(a.out + (size_t)(tail.tail_row + r) * kLatent) + 64 * half + lane;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
         __nv_bfloat162 x = __floats2bfloat162_rn(acc[j].x * inv, acc[j].y * inv);
         __nv_bfloat162 y = __floats2bfloat162_rn(acc[j].z * inv, acc[j].w * inv);
         out[32 * j] = make_uint2(*reinterpret_cast<uint32_t *>(&x), *reinterpret_cast<uint32_t *>(&y));
     }
-    if (lane == 0) a.lse[tail.tail_row + r] = den == 0.f ? -INFINITY : M * kLn2 + logf(den);
+    if (lane == 0 && half == 0) a.lse[tail.tail_row + r] = den == 0.f ? -INFINITY : M * kLn2 + logf(den);
 }
 
 static cudaError_t cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uint8_t *pool, int num_pages, int bytes,
@@ -1231,7 +1240,7 @@ static cudaError_t cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, const uin
 cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st)
 {
     static_assert(kDnSmem <= 232448, "shared memory budget");
-    static_assert(32 * kCombineRows >= kDensePairs, "one thread per cluster behind the tail");
+    static_assert(64 * kCombineRows >= kDensePairs, "one thread per cluster behind the tail");
     PFN_cuTensorMapEncodeTiled_v12000 encode;
     cudaError_t e = tensor_map_encoder(&encode);
     if (e != cudaSuccess) return e;
@@ -1242,8 +1251,10 @@ cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     e = launch_overlapped(dense_attn_kernel, dim3(2 * kDensePairs), dim3(kDnThreads), kDnSmem, st, maps, a);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(dense_combine_kernel, dim3(kDensePairs, kDenseRows / kCombineRows), dim3(32 * kCombineRows), 0,
-                             st, a);
+    // no row tile has more rows than the call
+    const long long most = a.rows * (long long)a.H < kDenseRows ? a.rows * (long long)a.H : kDenseRows;
+    return launch_overlapped(dense_combine_kernel, dim3(kDensePairs, (unsigned)((most + kCombineRows - 1) / kCombineRows)),
+                             dim3(64 * kCombineRows), 0, st, a);
 }
 
 }  // namespace csa
