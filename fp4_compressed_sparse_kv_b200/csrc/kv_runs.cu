@@ -4,13 +4,15 @@
 // KV, FP8 window) and section "先让长输入少走一半路" (the window holds the most recent tokens); yomxxx.com
 // long-form post, section 五 (addresses computed from the token index).
 //
-// Append: one warp per token, or four consecutive tokens per warp for long calls, as in pack.cu, whose
+// Append: one warp per token, or two consecutive tokens per warp for long calls, in the manner of pack.cu, whose
 // arithmetic (pack_token.cuh) it shares; the token's sequence, page, rotation and window slot are worked
 // out from its row number, so the caller builds no slot or angle arrays and no pass over the latents
 // comes before the pack.  Unpack: the inverse for the FP4 entries, e2m1 * e4m3 in bf16, which is exact
 // (at most 6 significant bits); a lane converts two pieces of 8 channels so that a warp's stores are
-// 512 contiguous bytes.  Both stream their bytes once and are bound by HBM for long calls, by the chain
-// of dependent metadata loads (cu_rows, then the page id, then the entry) for short ones.
+// 512 contiguous bytes.  Both stream their bytes once.  Long unpacks are bound by HBM (200,003 entries:
+// 44 us, 5.9 TB/s), long appends by the instructions of norm, rotation and pack (65,536 tokens: 45 us, 2.8 TB/s, about
+// 400 warp instructions a token), short calls by the chain of dependent metadata loads (cu_rows, then the page id, then
+// the entry), which the tokens of a warp share.
 #include "pack_token.cuh"
 #include "pipeline.cuh"
 #include "runs.cuh"
@@ -18,11 +20,13 @@
 namespace csa {
 
 constexpr int kRunWarps = 8;             // warps per CTA
-constexpr int kRunTokLarge = 4;          // tokens per warp of a long call
-constexpr int kRunLargeFrom = 4096;      // rows from which warps take kRunTokLarge tokens
+constexpr int kAppendTok = 2;            // tokens per warp of a long call: 32 warps of 64 registers on an SM (4 tokens in 98
+                                         // registers: 66 instead of 45 us for 65,536 tokens)
+constexpr int kUnpackTok = 4;            // 46 us for 200,003 entries (1: 54)
+constexpr int kRunLargeFrom = 4096;      // rows from which warps take several tokens
 
 template <bool kNorm, bool kRope, int kTok>
-__global__ void __launch_bounds__(32 * kRunWarps) kv_append_kernel(csa_kv_layer layer, Runs r,
+__global__ void __launch_bounds__(32 * kRunWarps, 4) kv_append_kernel(csa_kv_layer layer, Runs r,
                                                                    const uint16_t *__restrict__ latent,
                                                                    const uint16_t *__restrict__ idx_key,
                                                                    const float *__restrict__ norm_w,
@@ -45,24 +49,21 @@ __global__ void __launch_bounds__(32 * kRunWarps) kv_append_kernel(csa_kv_layer 
         }
     }
     RowPlace p[kTok];
+    warp_place_rows<kTok>(r, t0, layer.num_pages, p);
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
         const int t = t0 + i;
-        p[i].seq = -1;
-        if (t < r.rows) {
-            p[i] = warp_place_row(r, t, layer.num_pages);
-            if (kRope && p[i].pos >= rope_positions) {
-                p[i].bad = true;
-                p[i].seq = -1;
-            }
-            if (p[i].bad && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
-            in[i].s = p[i].slot;
-            in[i].ss = -1;
-            if (p[i].seq >= 0 && layer.swa && p[i].pos >= p[i].len - kWindow) {
-                const int row = r.swa_row[p[i].seq];
-                if (row >= 0 && row < layer.num_rows) in[i].ss = row * kWindow + p[i].pos % kWindow;
-                else if (row != -1 && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
-            }
+        if (kRope && p[i].pos >= rope_positions) {
+            p[i].bad = true;
+            p[i].seq = -1;
+        }
+        if (p[i].bad && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
+        in[i].s = p[i].slot;
+        in[i].ss = -1;
+        if (p[i].seq >= 0 && layer.swa && p[i].pos >= p[i].len - kWindow) {
+            const int row = r.swa_row[p[i].seq];
+            if (row >= 0 && row < layer.num_rows) in[i].ss = row * kWindow + p[i].pos % kWindow;
+            else if (row != -1 && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
         }
     }
 #pragma unroll
@@ -81,15 +82,13 @@ __global__ void __launch_bounds__(32 * kRunWarps) kv_unpack_kernel(csa_kv_layer 
     const int t0 = (blockIdx.x * kRunWarps + (threadIdx.x >> 5)) * kTok;
     const int lane = threadIdx.x & 31;
     if (t0 == 0 && lane == 0 && r.cu_rows[r.B] > r.rows) report(ws, CSA_ERR_DEVICE_DATA, r.B);
+    RowPlace p[kTok];
+    warp_place_rows<kTok>(r, t0, layer.num_pages, p);
     int64_t slot[kTok];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
-        slot[i] = -1;
-        if (t0 + i < r.rows) {
-            const RowPlace p = warp_place_row(r, t0 + i, layer.num_pages);
-            if (p.bad && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t0 + i);
-            if (p.seq >= 0) slot[i] = p.slot;
-        }
+        if (p[i].bad && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t0 + i);
+        slot[i] = p[i].seq >= 0 ? p[i].slot : -1;
     }
     // lane: channels 256 j + 8 lane .. + 7 for j = 0, 1
     uint32_t code[kTok][2];
@@ -125,8 +124,8 @@ static cudaError_t append(const csa_kv_layer &layer, const Runs &r, const uint16
                           const float *norm_w, const float *rope_table, int rope_positions, void *ws, cudaStream_t st)
 {
     if (r.rows >= kRunLargeFrom) {
-        const int per = kRunWarps * kRunTokLarge;
-        kv_append_kernel<kNorm, kRope, kRunTokLarge><<<(r.rows + per - 1) / per, 32 * kRunWarps, 0, st>>>(
+        const int per = kRunWarps * kAppendTok;
+        kv_append_kernel<kNorm, kRope, kAppendTok><<<(r.rows + per - 1) / per, 32 * kRunWarps, 0, st>>>(
             layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws);
     } else {
         kv_append_kernel<kNorm, kRope, 1><<<(r.rows + kRunWarps - 1) / kRunWarps, 32 * kRunWarps, 0, st>>>(
@@ -149,8 +148,8 @@ cudaError_t launch_kv_append(const csa_kv_layer &layer, const Runs &r, const uin
 cudaError_t launch_kv_unpack(const csa_kv_layer &layer, const Runs &r, uint16_t *latent, void *ws, cudaStream_t st)
 {
     if (r.rows >= kRunLargeFrom) {
-        const int per = kRunWarps * kRunTokLarge;
-        kv_unpack_kernel<kRunTokLarge><<<(r.rows + per - 1) / per, 32 * kRunWarps, 0, st>>>(layer, r, latent, ws);
+        const int per = kRunWarps * kUnpackTok;
+        kv_unpack_kernel<kUnpackTok><<<(r.rows + per - 1) / per, 32 * kRunWarps, 0, st>>>(layer, r, latent, ws);
     } else {
         kv_unpack_kernel<1><<<(r.rows + kRunWarps - 1) / kRunWarps, 32 * kRunWarps, 0, st>>>(layer, r, latent, ws);
     }

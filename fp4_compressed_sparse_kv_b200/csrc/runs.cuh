@@ -47,34 +47,50 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t *cu_rows, int B,
     return lo + __popc(__ballot_sync(0xffffffffu, lane < len && cu_rows[lo + min(lane + 1, len)] <= t));
 }
 
-// Place of row t (every lane of the warp gets it).
-__device__ __forceinline__ RowPlace warp_place_row(const Runs &r, int t, int num_pages)
+// Places of the warp's rows t0 .. t0 + kTok - 1 (every lane gets them): the sequence is looked up again only
+// where a row leaves it, and the page ids are loaded together, so a warp waits for one chain of loads, not kTok.
+template <int kTok>
+__device__ __forceinline__ void warp_place_rows(const Runs &r, int t0, int num_pages, RowPlace *p)
 {
-    RowPlace p;
-    p.seq = -1;
-    p.pos = p.len = 0;
-    p.slot = -1;
-    p.bad = false;
-    const int b = warp_find_sequence(r.cu_rows, r.B, t);
-    if (b >= r.B) return p;   // behind the last sequence
-    const int c0 = r.cu_rows[b], c1 = r.cu_rows[b + 1], L = r.seq_len[b];
-    if (t < c0 && b == 0) return p;   // before the first one
-    const bool holds = t >= c0 && t < c1 && c0 >= 0 && c1 <= r.rows;
-    const int n = holds ? c1 - c0 : 0;
-    if (!holds || L > r.max_seq_len || n > L) {
-        p.bad = true;
-        return p;
+    int b = -1, c0 = 0, c1 = 0, L = 0, page[kTok];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+        const int t = t0 + i;
+        p[i].seq = -1;
+        p[i].pos = p[i].len = 0;
+        p[i].slot = -1;
+        p[i].bad = false;
+        page[i] = 0;
+        if (t >= r.rows) continue;
+        if (b < 0 || t < c0 || t >= c1) {
+            b = warp_find_sequence(r.cu_rows, r.B, t);
+            if (b >= r.B) continue;           // behind the last sequence
+            c0 = r.cu_rows[b];
+            c1 = r.cu_rows[b + 1];
+            L = r.seq_len[b];
+        }
+        if (t < c0 && b == 0) continue;       // before the first one
+        const bool holds = t >= c0 && t < c1 && c0 >= 0 && c1 <= r.rows;
+        const int n = holds ? c1 - c0 : 0;
+        if (!holds || L > r.max_seq_len || n > L) {
+            p[i].bad = true;
+            continue;
+        }
+        p[i].pos = L - n + (t - c0);
+        p[i].len = L;
+        p[i].seq = b;
+        page[i] = r.block_table[(size_t)b * r.max_pages + p[i].pos / kPage];
     }
-    p.pos = L - n + (t - c0);
-    p.len = L;
-    const int page = r.block_table[(size_t)b * r.max_pages + p.pos / kPage];
-    if (page < 0 || page >= num_pages) {
-        p.bad = true;
-        return p;
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+        if (p[i].seq < 0) continue;
+        if (page[i] < 0 || page[i] >= num_pages) {
+            p[i].seq = -1;
+            p[i].bad = true;
+        } else {
+            p[i].slot = (int64_t)page[i] * kPage + p[i].pos % kPage;
+        }
     }
-    p.seq = b;
-    p.slot = (int64_t)page * kPage + p.pos % kPage;
-    return p;
 }
 
 }  // namespace csa

@@ -75,3 +75,31 @@ def test_binding_checks_shapes_and_types():
               dict(spans=torch.zeros(2, 2, dtype=torch.int32)), dict()):
         with pytest.raises(ValueError):
             csa.dense_attn(**{**good, **a})
+
+
+def test_pack_quotients_round_as_the_divisions_do():
+    """The pack's quotients (a product with the rounded reciprocal, then 11 significant bits, half up) land on the same
+    side of every border of E2M1 and E4M3 as the binary32 divisions x / s and amax / 6: every bf16 value, every scale."""
+    import numpy as np
+    x = (np.arange(0x7F81, dtype=np.uint32) << 16).view(np.float32)          # 0 .. infinity, one NaN
+
+    def near(a, inv):
+        with np.errstate(over="ignore", invalid="ignore"):
+            q = (a * inv).astype(np.float32)
+        return ((q.view(np.uint32) + np.uint32(0x1000)) & np.uint32(0xFFFFE000)).view(np.float32)
+
+    def nearest(y, grid):                                                    # index of the nearest, even index on a tie
+        mid = ((grid[1:].astype(np.float64) + grid[:-1]) / 2).astype(np.float32)
+        lo, hi = np.searchsorted(mid, y, side="left"), np.searchsorted(mid, y, side="right")
+        return np.where(lo == hi, lo, np.where(lo % 2 == 0, lo, hi))
+
+    e4m3 = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    e2m1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6], np.float32)
+    six = np.float32(6)
+    with np.errstate(over="ignore"):
+        assert np.array_equal(nearest(near(x[:-1], np.float32(1) / six), e4m3), nearest(x[:-1] / six, e4m3))
+        for s in e4m3[1:]:
+            inv = np.float32(1) / s
+            y, z = near(x, inv), x / s
+            assert np.array_equal(nearest(y[:-1], e2m1), nearest(z[:-1], e2m1)), s
+            assert np.isnan(y[-1]) and np.isnan(z[-1])
