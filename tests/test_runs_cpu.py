@@ -81,7 +81,7 @@ def test_pack_quotients_round_as_the_divisions_do():
     """The pack's quotients (a product with the rounded reciprocal, then 11 significant bits, half up) land on the same
     side of every border of E2M1 and E4M3 as the binary32 divisions x / s and amax / 6: every bf16 value, every scale."""
     import numpy as np
-    x = (np.arange(0x7F81, dtype=np.uint32) << 16).view(np.float32)          # 0 .. infinity, one NaN
+    x = (np.arange(0x7F82, dtype=np.uint32) << 16).view(np.float32)          # 0 .. infinity, one NaN
 
     def near(a, inv):
         with np.errstate(over="ignore", invalid="ignore"):
