@@ -407,7 +407,8 @@ csa_status csa_dense_attn(const csa_kv_layer *layer, const csa_batch *batch, con
         !aligned16(spans))
         return CSA_ERR_INVALID_ARG;
     if (H < 1 || H > 128) return CSA_ERR_UNSUPPORTED;
-    if (!(sm_scale > 0.f) || sm_scale > 1e30f || !(softcap >= 0.f) || softcap > 1e30f) return CSA_ERR_INVALID_ARG;
+    if (!(sm_scale > 0.f) || sm_scale > 1e30f) return CSA_ERR_INVALID_ARG;
+    if (softcap != 0.f && !(softcap >= 1e-20f && softcap <= 1e30f)) return CSA_ERR_INVALID_ARG;
     char *base = (char *)ws;
     DenseArgs a;
     a.codes = layer->codes;

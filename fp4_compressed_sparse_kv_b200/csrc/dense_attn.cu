@@ -155,6 +155,7 @@ __device__ __forceinline__ void tile_pages(const DenseArgs &a, int c0, int n, in
     if (a.spans) {
         lo = L;
         hi = 0;
+#pragma unroll 8
         for (int t = ta; t <= tb; ++t) {
             const int2 s = a.spans[c0 + t];
             const int sl = max(s.x, 0), sh = min(s.y, L);
@@ -390,7 +391,8 @@ __device__ __forceinline__ void stage_q(const DenseArgs &a, DenseMisc &ms, const
 #pragma unroll
         for (int m = 0; m < 4; ++m) h[m] = pack_f16x2(bf16_lo(ww[m]) * sc, bf16_hi(ww[m]) * sc);
         *reinterpret_cast<uint4 *>(stage + i * 512 + ((lane ^ (i & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (lane == 0) ms.zs[i] = a.sm_scale * __int_as_float((127 - k) << 23) * kLog2e;
+        // a row of non-finite q is NaN whatever its products are
+        if (lane == 0) ms.zs[i] = top >= 0x7F800000u ? __int_as_float(0x7FC00000) : a.sm_scale * __int_as_float((127 - k) << 23) * kLog2e;
     }
 }
 

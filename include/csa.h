@@ -414,7 +414,7 @@ csa_status csa_kv_unpack_fp4(const csa_kv_layer *layer, const csa_batch *batch, 
  * csa_dense_attn -- attention of a run's query rows over every visible position of the FP4 cache (no
  * selection, no window ring): for head h of row t at position p, over the positions j it sees,
  *     s_j = sm_scale * q_h . v_j
- *     s_j = softcap * tanh(s_j / softcap)      if softcap > 0
+ *     s_j = softcap * tanh(s_j / softcap)      if softcap > 0 (1e-20 .. 1e30)
  *     s_j = s_j - slopes[h] * |p - j|          if slopes
  *     out_h = sum_j e^{s_j} v_j / sum_j e^{s_j},  lse_h = log sum_j e^{s_j}
  *   q        bf16 [rows][H][512], 1 <= H <= 128
@@ -423,8 +423,8 @@ csa_status csa_kv_unpack_fp4(const csa_kv_layer *layer, const csa_batch *batch, 
  *            causal, (0, p + 1).  A span holds a sliding window, the row's document in a packed sequence,
  *            a prefix seen in both directions; one with lo >= hi sees nothing: out = 0, lse = -inf.
  *   out      bf16 [rows][H][512], lse float [rows][H]
- * fp16 operands (exact for the entries; q scaled by a power of two per row), fp32 accumulation and sums,
- * probabilities rounded to fp16 once, out rounded to bf16 once.  Rows of non-finite q, and rows that see an
+ * fp16 operands (exact for the entries; q scaled by a power of two per row and half of the channels), fp32
+ * accumulation and sums, probabilities rounded to fp16 once, out rounded to bf16 once.  Rows of non-finite q, and rows that see an
  * entry with a NaN scale, give NaN; no other row does.  Results do not depend on timing, but rounding
  * depends on how the call's rows divide over the GPU.  Every position of a bad page is left out.
  * ws: csa_dense_attn_workspace_bytes() bytes, whatever the sizes.

@@ -360,3 +360,72 @@ def test_append_attend_unpack_together():
     assert torch.equal(back.double(), torch.from_numpy(oracle.dequant_main(ref["codes"], ref["scales"])).double().cuda())
     got = [torch.cat([o[i] for o in outs]) for i in range(2)]
     assert_close(got, reference(layer, whole, q, None, 0.0, None))
+
+
+def test_as_many_sequences_as_a_batch_holds():
+    """16,384 sequences, most without a row: the division's tables fill the shared memory they are given."""
+    B = 16384
+    rng = np.random.default_rng(50)
+    n = np.where(rng.random(B) < 0.05, 1, 0)
+    n[[0, 7000, B - 1]] = [2, 40, 3]
+    lens = np.where(n > 0, rng.integers(1, 100, B), 1) + n
+    r = Run(n.tolist(), lens.tolist(), 51)
+    layer = random_layer(r.num_pages, 52)
+    q = queries(r.rows, 8, 53)
+    got = attend(layer, r, q)
+    assert csa.check_device_error(got[2])[0] == 0
+    assert_close(got, reference(layer, r, q, None, 0.0, None))
+
+
+@pytest.mark.parametrize("H,n,L", [(1, 700, 1000), (3, 500, 700), (128, 9, 9)])
+def test_spans_of_many_tokens_in_one_row_tile(H, n, L):
+    """Up to 128 tokens share a row tile; each has its own span, some see nothing, whole tiles among them."""
+    r = Run([n], [L], 54 + H)
+    layer = random_layer(r.num_pages, 55 + H)
+    q = queries(n, H, 56 + H)
+    rng = np.random.default_rng(57 + H)
+    lo = rng.integers(-5, L, n)
+    s = np.stack([lo, np.minimum(lo + rng.integers(0, 200, n), L + 3)], 1)
+    s[n // 3:n // 3 + 260] = 11                              # two row tiles in a row that see nothing (one head)
+    spans = torch.from_numpy(s.astype(np.int32)).cuda()
+    got = attend(layer, r, q, spans, cap=5.0)
+    assert csa.check_device_error(got[2])[0] == 0
+    assert_close(got, reference(layer, r, q, spans, 5.0, None))
+
+
+def test_non_finite_queries_under_a_cap():
+    """The cap maps infinite scores to finite ones; a row of infinite q is NaN all the same, and only that row."""
+    r = Run([4], [150], 58)
+    layer = random_layer(r.num_pages, 59)
+    layer.codes |= 0x11                                      # no zero among the entries' values
+    q = queries(4, 16, 60)
+    clean = reference(layer, r, q, None, 3.0, None)
+    q[1, 5] = math.inf
+    q[2, 0, 300] = -math.inf
+    got = attend(layer, r, q, cap=3.0)
+    sick = torch.zeros((4, 16), dtype=torch.bool, device="cuda")
+    sick[1, 5] = sick[2, 0] = True
+    assert torch.isnan(got[0][sick].float()).all() and torch.isnan(got[1][sick]).all()
+    assert_close([x[~sick][None] for x in got[:2]], [x[~sick][None] for x in clean])
+
+
+def test_other_streams_workspaces_and_orders():
+    """The caller's stream argument; one workspace for calls of different sizes in turn, many times over."""
+    runs = [Run([1], [3000], 61), Run([33, 0, 90], [400, 5, 90], 62), Run([1] * 20, [700] * 20, 63)]
+    layers = [random_layer(r.num_pages, 64 + i) for i, r in enumerate(runs)]
+    qs = [queries(r.rows, 40, 66 + i) for i, r in enumerate(runs)]
+    want = [attend(l, r, q)[:2] for l, r, q in zip(layers, runs, qs)]
+    torch.cuda.synchronize()
+    side, ws = torch.cuda.Stream(), csa.dense_attn_workspace()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for l, r, q in zip(layers, runs, qs):
+            out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+            side.wait_stream(torch.cuda.current_stream())
+            csa.dense_attn(l, r.batch, r.cu_rows, q, out, lse, ws, stream=side)
+            outs.append((out, lse))
+    side.synchronize()
+    for i, (out, lse) in enumerate(outs):
+        assert torch.equal(out, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
+    assert csa.check_device_error(ws)[0] == 0

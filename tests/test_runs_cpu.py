@@ -103,3 +103,33 @@ def test_pack_quotients_round_as_the_divisions_do():
             y, z = near(x, inv), x / s
             assert np.array_equal(nearest(y[:-1], e2m1), nearest(z[:-1], e2m1)), s
             assert np.isnan(y[-1]) and np.isnan(z[-1])
+
+
+def test_softcap_has_a_range(lib):
+    l, b, lay, bat = handles()
+    f = lambda cap, rows: lib.csa_dense_attn(l, b, OK, rows, OK, 64, 0.1, cap, None, None, OK, OK, OK, BIG, None)
+    for cap in (1e-21, -1e-21, 1e31):
+        assert f(cap, 4) == 1, cap
+        assert f(cap, 0) == 0, cap                           # no rows: nothing is looked at
+
+
+def test_arrays_of_a_run_are_on_the_current_device(monkeypatch):
+    """Tensors of another device than the current one are refused before anything is launched (devices faked)."""
+    from fp4_compressed_sparse_kv_b200 import csa
+
+    class On:
+        def __init__(self, device):
+            self.device_index = device
+
+        def get_device(self):
+            return self.device_index
+
+    monkeypatch.setattr(csa.torch, "Tensor", On)
+    monkeypatch.setattr(csa.torch.cuda, "current_device", lambda: 0)
+    assert csa._run_device(On(0), "ws") == 0
+    with pytest.raises(ValueError, match="not the current one"):
+        csa._run_device(On(1), "ws")
+    monkeypatch.setattr(csa, "_ptr", lambda t, name: 1)
+    with pytest.raises(ValueError, match="not on the current device"):
+        csa._run_ptr(On(1), "latent", 0)
+    assert csa._run_ptr(None, "slopes", 0) == 0
