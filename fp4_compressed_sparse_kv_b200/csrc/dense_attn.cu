@@ -68,6 +68,7 @@ constexpr uint32_t kDnColQ = 256;                // Q_x: 256 channels, two per c
 constexpr uint32_t kDnColS = 384;                // S_x of tile g: columns 384 + 64(g%2) ..
 constexpr long long kDnMinTiles = 4;             // pages a cluster takes at least (one row tile of 64 pages: 27.5 us; 2: 30.7)
 constexpr int kDnPieceCost = 8;                  // what a row tile costs besides its pages, in pages
+constexpr float kDnNoMax = -3.402823466e38f;     // reference of a row that has seen nothing: no finite score is below it
 static_assert(kTile == kPage, "a tile is one page");
 static_assert(kDnStages * kDnVBuf >= kDenseRows * kDnCh * 2, "Q is staged in the V buffers");
 
@@ -756,7 +757,7 @@ __device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_se
     const uint32_t r_free_there = remote_addr(smem_addr(&ms.r_free[grp][q]), peer);
     uint32_t sent = n_sent;
     bool ok = true;
-    float m_run = kNoMax;                    // the reference of this thread's sum (log2 domain)
+    float m_run = kDnNoMax;                    // the reference of this thread's sum (log2 domain)
     float lsum = 0.f;                        // its share of the row's denominator
 #pragma unroll 1
     for (int t = (int)((uint32_t)(grp + kDnGroups - (int)(g0 % kDnGroups)) % kDnGroups); t < nk; t += kDnGroups) {
@@ -838,7 +839,7 @@ __device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_se
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
             // the row's reference after the previous tile, which another group has; it grows only by more
             // than 2^8 at a time
-            float m_old = kNoMax;
+            float m_old = kDnNoMax;
             if (t > 0) {
                 const uint32_t gp = g - 1u;
                 ok = warp_wait_hint(&ms.m_full[gp % kDnGroups][q], (gp / kDnGroups) & 1u, cx, 18);
@@ -849,7 +850,7 @@ __device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_se
             if (u == 0) ms.m_row[grp][hr] = m_new;
             __syncwarp();
             lane0_arrive(&ms.m_full[grp][q], lane);
-            al = ex2(m_old - m_new);        // 0 while m_old is kNoMax, 1 if unchanged
+            al = ex2(m_old - m_new);        // 0 while m_old is kDnNoMax, 1 if unchanged
             lsum *= ex2(m_run - m_new);
             m_run = m_new;
         } else {                            // the barrier's phases count tiles
@@ -897,7 +898,7 @@ __device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_se
     if (u == 0) ms.ml[grp][hr] = make_float2(m_run, lsum);
     bar_sync(1 + q, 32 * kDnGroups);
     if (grp == 0) {
-        float M = kNoMax, l = 0.f;
+        float M = kDnNoMax, l = 0.f;
 #pragma unroll
         for (int i = 0; i < kDnGroups; ++i) M = fmaxf(M, ms.ml[i][hr].x);
 #pragma unroll

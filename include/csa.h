@@ -398,7 +398,8 @@ csa_status csa_kv_import(const csa_kv_layer *layer, const int32_t *block_table, 
  *     norm_weight    float [512], or NULL: the latent is normalised already
  *     rope_table     float [rope_positions][32][2] (cos, sin) of every position, or NULL: rotated already
  *   RMSNorm, rotation, rounding to bf16 and pack are bit for bit those of csa_kv_norm_rope_pack_fp4 (with
- *   both NULL, of csa_kv_pack_fp4).  ws needs CSA_WORKSPACE_HEADER_BYTES.
+ *   both NULL, of csa_kv_pack_fp4).  No two rows may have the same place: sequences that share a page or a
+ *   window row append to it in separate calls.  ws needs CSA_WORKSPACE_HEADER_BYTES.
  *
  * csa_kv_unpack_fp4 -- the run's FP4 entries as values, latent bf16 [rows][512] = e2m1(code) * e4m3(scale)
  *   (exact).  With n_b = seq_len[b] it reads a whole context.  ws needs CSA_WORKSPACE_HEADER_BYTES.

@@ -429,3 +429,33 @@ def test_other_streams_workspaces_and_orders():
     for i, (out, lse) in enumerate(outs):
         assert torch.equal(out, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
     assert csa.check_device_error(ws)[0] == 0
+
+
+@pytest.mark.parametrize("width", [1, 2, 2500])
+def test_scores_of_large_magnitude(width):
+    """Slopes, or a scale, that put every visible score below -2^100: the largest score takes all of the weight, so out
+    is that entry (its product with a power of two and the division by it are exact) and lse that score."""
+    n, L, H = 5, 2600, 6
+    r = Run([n], [L], 70)
+    layer = random_layer(r.num_pages, 71)
+    v = values64(layer, r.slots(0, np.arange(L)))
+    pos = np.arange(L - n, L)
+    hi = pos - np.array([0, 1, 5, 63, 64])                   # the row's own position is not among those it sees
+    s = np.stack([hi - width, hi], 1)
+    spans = torch.from_numpy(s.astype(np.int32)).cuda()
+    slopes = 2.0 ** (101 + torch.arange(H, device="cuda").float())
+    got = attend(layer, r, queries(n, H, 72), spans, slopes=slopes)
+    nearest = torch.from_numpy(hi - 1).cuda()
+    want = v[nearest][:, None].expand(n, H, 512)
+    lse = -slopes.double()[None] * torch.from_numpy(pos - hi + 1).cuda()[:, None]
+    assert torch.equal(got[0].double(), want)
+    assert float(((got[1].double() - lse) / lse).abs().max()) <= 2.0 ** -20     # the scores vanish beside the bias
+    # the same by the scale: q opposite to the entry, which is at least 2^100 of the score away from zero
+    q = -(v[nearest][:, None] * 2.0 ** torch.arange(H, device="cuda")[:, None]).bfloat16()
+    one = torch.stack([nearest, nearest + 1], 1).int()
+    got = attend(layer, r, q, one, sm_scale=1e30)
+    assert torch.equal(got[0].double(), want)
+    lse = 1e30 * (q.double() * v[nearest][:, None]).sum(-1)
+    assert float(lse.max()) < -1e32
+    assert float(((got[1].double() - lse) / lse).abs().max()) <= 2.0 ** -15     # terms of one sign: 512 roundings
+    assert csa.check_device_error(got[2])[0] == 0
