@@ -21,13 +21,21 @@
 // scaled by a power of two per row and channel half, so a row of very large or non-finite values does not
 // touch the others of its tile.  O is rescaled only when a row's maximum has grown by 2^8.
 //
-// Work division: the (row tile, page) pairs of the whole call, row tile by row tile, are one line that
-// the 74 persistent clusters (one CTA per SM) cut into equal shares, whatever the batch looks like: one long
-// sequence splits over all SMs, a prefill chunk gives each cluster whole row tiles.  Every CTA works out the
-// division itself from cu_rows, seq_len and the spans (a block scan; no extra launch).  A cluster finishes
-// the row tiles it holds whole; the first and last tile of its share may be shared with its neighbours,
-// and those leave an fp32 partial (unnormalised O, running maximum and sum) in the workspace, which the
-// combine kernel adds in cluster order, so results do not depend on timing.
+// Work division: the (row tile, page) pairs of the whole call, row tile by row tile, are one line (on which a row
+// tile also takes the length of kDnPieceCost pages) that the 74 persistent clusters, one CTA per SM, cut into equal
+// shares, whatever the batch looks like: one long sequence splits over all SMs, a prefill chunk gives each cluster
+// whole row tiles.  Every CTA works out the division itself from cu_rows, seq_len and the spans (a block scan; no extra
+// launch).  A cluster finishes the row tiles it holds whole; the first and last tile of its share may be shared with
+// its neighbours, and those leave an fp32 partial (unnormalised O, running maximum and sum) in the workspace, which
+// the combine kernel adds in cluster order, so results do not depend on timing.
+//
+// What bounds it.  A (row tile, page) pair needs 1,036 tensor cycles (QK 512, PV 524); it takes about 2,300, which is
+// half of the softmax's chain (read S, send, receive, maximum, exp2, P to both CTAs, PV, P buffer free: 4,600 cycles):
+// two groups of warps take the tiles in turn, and a third does not fit the two S and P buffers that TMEM and shared
+// memory leave.  A row tile costs 16,000 cycles more (Q into TMEM, the last tiles' chain, O out), and a call 15 us before
+// and after (plan, first pages, partials, combine).  Measured: 2,048 rows of 64 heads behind 14,336 positions 4.2-4.4 ms
+// (1.0 PFLOP/s, at the power limit); one row of each of 8 sequences of 131,072 positions, 64 heads (half of the tensor
+// rows idle): 270 us; one row of 16 heads over 4,096 positions: 23 us.
 #include <cuda_bf16.h>
 
 #include "attention_tile.cuh"
