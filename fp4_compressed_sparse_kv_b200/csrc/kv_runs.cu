@@ -4,15 +4,14 @@
 // KV, FP8 window) and section "先让长输入少走一半路" (the window holds the most recent tokens); yomxxx.com
 // long-form post, section 五 (addresses computed from the token index).
 //
-// Append: one warp per token, or two consecutive tokens per warp for long calls, in the manner of pack.cu, whose
-// arithmetic (pack_token.cuh) it shares; the token's sequence, page, rotation and window slot are worked
-// out from its row number, so the caller builds no slot or angle arrays and no pass over the latents
-// comes before the pack.  Unpack: the inverse for the FP4 entries, e2m1 * e4m3 in bf16, which is exact
+// Append: one warp per token, with the arithmetic of pack.cu (pack_token.cuh); the token's sequence, page,
+// rotation and window slot are worked out from its row number, so the caller builds no slot or angle
+// arrays and no pass over the latents comes before the pack.  Unpack: the inverse for the FP4 entries, e2m1 * e4m3 in bf16, which is exact
 // (at most 6 significant bits); a lane converts two pieces of 8 channels so that a warp's stores are
 // 512 contiguous bytes.  Both stream their bytes once.  Long unpacks are bound by HBM (200,003 entries:
-// 44 us, 5.9 TB/s), long appends by the instructions of norm, rotation and pack (65,536 tokens: 45 us, 2.8 TB/s, about
+// 44 us, 5.9 TB/s), long appends by the instructions of norm, rotation and pack (65,536 tokens: 42 us, 3.0 TB/s, about
 // 400 warp instructions a token), short calls by the chain of dependent metadata loads (cu_rows, then the page id, then
-// the entry), which the tokens of a warp share.
+// the entry), which the tokens of an unpacking warp share.
 #include "pack_token.cuh"
 #include "pipeline.cuh"
 #include "runs.cuh"
@@ -20,13 +19,13 @@
 namespace csa {
 
 constexpr int kRunWarps = 8;             // warps per CTA
-constexpr int kAppendTok = 2;            // tokens per warp of a long call: 32 warps of 64 registers on an SM (4 tokens in 98
-                                         // registers: 66 instead of 45 us for 65,536 tokens)
-constexpr int kUnpackTok = 4;            // 46 us for 200,003 entries (1: 54)
-constexpr int kRunLargeFrom = 4096;      // rows from which warps take several tokens
+constexpr int kUnpackTok = 4;            // tokens per unpacking warp: 46 us for 200,003 entries (1: 54)
+constexpr int kRunLargeFrom = 4096;      // rows from which unpacking warps take several tokens
 
-template <bool kNorm, bool kRope, int kTok>
-__global__ void __launch_bounds__(32 * kRunWarps, 4) kv_append_kernel(csa_kv_layer layer, Runs r,
+// 40 warps on an SM hide a token's chain of conversions and shuffles better than several tokens per warp do: 65,536
+// tokens 42 us (2 tokens per warp, 32 warps: 45; 4 tokens in 98 registers: 66).
+template <bool kNorm, bool kRope>
+__global__ void __launch_bounds__(32 * kRunWarps, 5) kv_append_kernel(csa_kv_layer layer, Runs r,
                                                                    const uint16_t *__restrict__ latent,
                                                                    const uint16_t *__restrict__ idx_key,
                                                                    const float *__restrict__ norm_w,
@@ -34,45 +33,29 @@ __global__ void __launch_bounds__(32 * kRunWarps, 4) kv_append_kernel(csa_kv_lay
                                                                    int rope_positions, void *ws)
 {
     grid_dep_launch();   // a dependent kernel waits for this grid before it reads the caches
-    const int t0 = (blockIdx.x * kRunWarps + (threadIdx.x >> 5)) * kTok;
+    const int t = blockIdx.x * kRunWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (t0 == 0 && lane == 0 && r.cu_rows[r.B] > r.rows) report(ws, CSA_ERR_DEVICE_DATA, r.B);
-    PackIn in[kTok];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        const int t = t0 + i;
-        if (t < r.rows) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(latent + (size_t)t * kLatent) + 2 * lane;
-            in[i].a = src[0];
-            in[i].b = src[1];
-            in[i].kw = reinterpret_cast<const uint2 *>(idx_key + (size_t)t * kIdxDim)[lane];
-        }
+    if (t == 0 && lane == 0 && r.cu_rows[r.B] > r.rows) report(ws, CSA_ERR_DEVICE_DATA, r.B);
+    if (t >= r.rows) return;
+    PackIn in;
+    const uint4 *src = reinterpret_cast<const uint4 *>(latent + (size_t)t * kLatent) + 2 * lane;
+    in.a = src[0];
+    in.b = src[1];
+    in.kw = reinterpret_cast<const uint2 *>(idx_key + (size_t)t * kIdxDim)[lane];
+    RowPlace p[1];
+    warp_place_rows<1>(r, t, layer.num_pages, p);
+    const bool no_rotation = kRope && p[0].pos >= rope_positions;
+    if ((p[0].bad || no_rotation) && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
+    if (p[0].seq < 0 || no_rotation) return;
+    in.s = p[0].slot;
+    in.ss = -1;
+    if (layer.swa && p[0].pos >= p[0].len - kWindow) {
+        const int row = r.swa_row[p[0].seq];
+        if (row >= 0 && row < layer.num_rows) in.ss = row * kWindow + p[0].pos % kWindow;
+        else if (row != -1 && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
     }
-    RowPlace p[kTok];
-    warp_place_rows<kTok>(r, t0, layer.num_pages, p);
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        const int t = t0 + i;
-        if (kRope && p[i].pos >= rope_positions) {
-            p[i].bad = true;
-            p[i].seq = -1;
-        }
-        if (p[i].bad && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
-        in[i].s = p[i].slot;
-        in[i].ss = -1;
-        if (p[i].seq >= 0 && layer.swa && p[i].pos >= p[i].len - kWindow) {
-            const int row = r.swa_row[p[i].seq];
-            if (row >= 0 && row < layer.num_rows) in[i].ss = row * kWindow + p[i].pos % kWindow;
-            else if (row != -1 && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kTok; ++i)
-        if (p[i].seq >= 0)
-            pack_token<kNorm, kRope>(layer, in[i], t0 + i, lane, ws, norm_w,
-                                     kRope ? rope_table + (size_t)p[i].pos * kRopeRow : nullptr);
+    pack_token<kNorm, kRope>(layer, in, t, lane, ws, norm_w, kRope ? rope_table + (size_t)p[0].pos * kRopeRow : nullptr);
 }
-
 
 template <int kTok>
 __global__ void __launch_bounds__(32 * kRunWarps) kv_unpack_kernel(csa_kv_layer layer, Runs r,
@@ -123,14 +106,8 @@ template <bool kNorm, bool kRope>
 static cudaError_t append(const csa_kv_layer &layer, const Runs &r, const uint16_t *latent, const uint16_t *idx_key,
                           const float *norm_w, const float *rope_table, int rope_positions, void *ws, cudaStream_t st)
 {
-    if (r.rows >= kRunLargeFrom) {
-        const int per = kRunWarps * kAppendTok;
-        kv_append_kernel<kNorm, kRope, kAppendTok><<<(r.rows + per - 1) / per, 32 * kRunWarps, 0, st>>>(
-            layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws);
-    } else {
-        kv_append_kernel<kNorm, kRope, 1><<<(r.rows + kRunWarps - 1) / kRunWarps, 32 * kRunWarps, 0, st>>>(
-            layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws);
-    }
+    kv_append_kernel<kNorm, kRope><<<(r.rows + kRunWarps - 1) / kRunWarps, 32 * kRunWarps, 0, st>>>(
+        layer, r, latent, idx_key, norm_w, rope_table, rope_positions, ws);
     return cudaGetLastError();
 }
 
