@@ -3,20 +3,24 @@
     python -m fp4_compressed_sparse_kv_b200.build [--verbose-ptxas]
 
 Each .cu under csrc/ is compiled to an object under _build/ and linked with a static CUDA runtime,
-so the shared object loads wherever the NVIDIA driver is present.
+so the shared object loads wherever the NVIDIA driver is present.  csrc/run_binding.cpp, argument marshalling of the
+Python binding against PyTorch's headers, becomes _runs.so.
 """
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libcsa.so")
+RUNS = os.path.join(HERE, "_runs.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -46,6 +50,24 @@ def _compile(src, verbose_ptxas):
     return obj, r.stderr
 
 
+def _build_binding():
+    src = os.path.join(CSRC, "run_binding.cpp")
+    deps = [src, os.path.join(INCLUDE, "csa.h")]
+    if os.path.exists(RUNS) and os.path.getmtime(RUNS) >= max(os.path.getmtime(d) for d in deps):
+        return
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = RUNS + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Werror", "-I", INCLUDE]
+    for inc in (os.path.join(torch, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-isystem", inc]
+    cmd += [src, "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
+    os.replace(tmp, RUNS)
+
+
 def build(verbose_ptxas: bool = False, quiet: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -64,6 +86,7 @@ def build(verbose_ptxas: bool = False, quiet: bool = True) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
         os.replace(tmp, LIB)
+    _build_binding()
     return LIB
 
 

@@ -415,8 +415,27 @@ def kv_import(layer, block_table, n, src, ws, stream=None):
            "csa_kv_import")
 
 
-# The calls over ragged runs are short enough that their arguments' marshalling counts: the layer and the
-# batch are packed as bytes laid out like KVLayerC and BatchC, which costs a third of a ctypes structure.
+_runs_mod = None
+
+
+def _runs():
+    """The extension that checks and marshals the arguments of append and read-back, bound to the library.  Their
+    kernels run 2 to 4 us for a decode step, and marshalling in Python alone took 5."""
+    global _runs_mod
+    if _runs_mod is None:
+        L = lib()
+        try:
+            from . import _runs as mod
+        except ImportError as e:
+            raise RuntimeError("_runs.so is missing or does not load: build it with "
+                               "python -m fp4_compressed_sparse_kv_b200.build") from e
+        mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.csa_kv_append_fp4, L.csa_kv_unpack_fp4)))
+        _runs_mod = mod
+    return _runs_mod
+
+
+# The attention's layer and batch are packed as bytes laid out like KVLayerC and BatchC, which costs a third of a
+# ctypes structure.
 _pack_layer = struct.Struct("=5Q2i").pack
 _pack_batch = struct.Struct("=i4xQQi4xQi4x").pack
 
@@ -466,33 +485,13 @@ def kv_append_fp4(layer, batch, cu_rows, latent, idx_key, ws, norm_weight=None, 
     (bf16 [rows, 512]) and idx_key (bf16 [rows, 128]) are the last positions of sequence b (batch.seq_len
     counts them).  norm_weight float32 [512] and rope_table float32 [positions, 32, 2] of (cos, sin) apply
     RMSNorm and the rotation of each row's position first; the last 128 positions also go to the window."""
-    rows = latent.shape[0]
-    _run_rows(batch, cu_rows)
-    _run_array(latent, "latent", torch.bfloat16, (rows, LATENT))
-    _run_array(idx_key, "idx_key", torch.bfloat16, (rows, IDX_DIM))
-    if norm_weight is not None:
-        _run_array(norm_weight, "norm_weight", torch.float32, (LATENT,))
-    positions = 0
-    if rope_table is not None:
-        positions = rope_table.shape[0]
-        _run_array(rope_table, "rope_table", torch.float32, (positions, 32, 2))
-    dev, p = _run_device(ws, "ws"), _run_ptr
-    lc, bc = _run_handles(layer, batch, dev)
-    _check(lib().csa_kv_append_fp4(lc, bc, p(cu_rows, "cu_rows", dev), rows, p(latent, "latent", dev),
-                                   p(idx_key, "idx_key", dev), p(norm_weight, "norm_weight", dev),
-                                   p(rope_table, "rope_table", dev), positions, p(ws, "ws", dev), ws.numel(),
-                                   _stream(stream)), "csa_kv_append_fp4")
+    _check(_runs().kv_append_fp4(layer, batch, cu_rows, latent, idx_key, ws, norm_weight, rope_table, stream),
+           "csa_kv_append_fp4")
 
 
 def kv_unpack_fp4(layer, batch, cu_rows, latent, ws, stream=None):
     """Read a ragged run's FP4 entries back as values into latent, bf16 [rows, 512] (exact)."""
-    rows = latent.shape[0]
-    _run_rows(batch, cu_rows)
-    _run_array(latent, "latent", torch.bfloat16, (rows, LATENT))
-    dev, p = _run_device(ws, "ws"), _run_ptr
-    lc, bc = _run_handles(layer, batch, dev)
-    _check(lib().csa_kv_unpack_fp4(lc, bc, p(cu_rows, "cu_rows", dev), rows, p(latent, "latent", dev), p(ws, "ws", dev),
-                                   ws.numel(), _stream(stream)), "csa_kv_unpack_fp4")
+    _check(_runs().kv_unpack_fp4(layer, batch, cu_rows, latent, ws, stream), "csa_kv_unpack_fp4")
 
 
 def dense_attn_workspace(device="cuda", stream=None):

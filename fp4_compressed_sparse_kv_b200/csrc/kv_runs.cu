@@ -10,7 +10,7 @@
 // (at most 6 significant bits); a lane converts two pieces of 8 channels so that a warp's stores are
 // 512 contiguous bytes.  Both stream their bytes once.  Long unpacks are bound by HBM (200,003 entries:
 // 44 us, 5.9 TB/s), long appends by the instructions of norm, rotation and pack (65,536 tokens: 42 us, 3.0 TB/s, about
-// 400 warp instructions a token), short calls by the chain of dependent metadata loads (cu_rows, then the page id, then
+// 460 warp instructions a token), short calls by the chain of dependent metadata loads (cu_rows, then the page id, then
 // the entry), which the tokens of an unpacking warp share.
 #include "pack_token.cuh"
 #include "pipeline.cuh"

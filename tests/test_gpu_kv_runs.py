@@ -194,3 +194,52 @@ def test_captured_and_replayed_on_another_stream():
     torch.cuda.synchronize()
     ref = oracle.pack_tokens(lat ^ np.uint16(0x8000), key)
     assert torch.equal(out.double(), torch.from_numpy(oracle.dequant_main(ref["codes"], ref["scales"])).double().cuda())
+
+
+def test_binding_refuses_and_takes_streams_and_threads():
+    """Non-contiguous and host tensors are refused with nothing written; a side stream and two host threads at once give
+    the same entries."""
+    import threading
+    r = Run([5, 70], [9, 100], 81)
+    g = torch.Generator(device="cuda").manual_seed(82)
+    latent = torch.randn((75, 512), generator=g, device="cuda").bfloat16()
+    key = torch.randn((75, 128), generator=g, device="cuda").bfloat16()
+    new_ws = lambda: torch.zeros(csa.HEADER_BYTES, dtype=torch.uint8, device="cuda")
+    want, ws = csa.KVLayer(r.num_pages, 2), new_ws()
+    csa.workspace_init(ws)
+    wide = torch.zeros((75, 1024), dtype=torch.bfloat16, device="cuda")[:, ::2]
+    for bad in (dict(latent=wide), dict(idx_key=key.cpu()), dict(cu_rows=r.cu_rows.cpu()), dict(norm_weight=torch.ones(512))):
+        with pytest.raises(ValueError):
+            csa.kv_append_fp4(**{**dict(layer=want, batch=r.batch, cu_rows=r.cu_rows, latent=latent, idx_key=key, ws=ws), **bad})
+    with pytest.raises(ValueError):
+        csa.kv_unpack_fp4(want, r.batch, r.cu_rows, wide, ws)
+    assert not want.codes.any() and not wide.any()
+    csa.kv_append_fp4(want, r.batch, r.cu_rows, latent, key, ws)
+    assert csa.check_device_error(ws)[0] == 0
+    torch.cuda.synchronize()
+    layers = [csa.KVLayer(r.num_pages, 2) for _ in range(4)]
+    outs = [torch.zeros_like(latent) for _ in range(4)]
+    spaces = [new_ws() for _ in range(4)]
+    for w in spaces:
+        csa.workspace_init(w)
+    torch.cuda.synchronize()
+
+    def work(i):
+        side = torch.cuda.Stream()
+        for _ in range(50):
+            csa.kv_append_fp4(layers[i], r.batch, r.cu_rows, latent, key, spaces[i], stream=side)
+            csa.kv_unpack_fp4(layers[i], r.batch, r.cu_rows, outs[i], spaces[i], stream=side)
+        side.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    back = torch.zeros_like(latent)
+    csa.kv_unpack_fp4(want, r.batch, r.cu_rows, back, ws)
+    for l, o, w in zip(layers, outs, spaces):
+        assert csa.check_device_error(w)[0] == 0
+        for name in ("codes", "scales", "keys", "swa", "swa_scale"):
+            assert torch.equal(getattr(l, name), getattr(want, name)), name
+        assert torch.equal(o, back)

@@ -133,3 +133,36 @@ def test_arrays_of_a_run_are_on_the_current_device(monkeypatch):
     with pytest.raises(ValueError, match="not on the current device"):
         csa._run_ptr(On(1), "latent", 0)
     assert csa._run_ptr(None, "slopes", 0) == 0
+
+
+def test_binding_of_append_and_unpack_refuses_before_the_library_is_called():
+    """The extension's own checks: what is no tensor, a workspace on the CPU, lengths that do not fit, missing attributes,
+    a wrong number of arguments."""
+    from fp4_compressed_sparse_kv_b200 import csa
+    mod = csa._runs()
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    layer = csa.KVLayer(2, 1, device="cpu")
+    batch = csa.Batch(torch.zeros(1, dtype=torch.int32), torch.zeros((1, 2), dtype=torch.int32),
+                      torch.zeros(1, dtype=torch.int32), 128)
+    cu, ws = torch.zeros(2, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    good = dict(layer=layer, batch=batch, cu_rows=cu, latent=bf(3, 512), idx_key=bf(3, 128), ws=ws)
+    for a in (dict(latent=[1.0]), dict(idx_key=None), dict(cu_rows=(0, 3)), dict(ws=b"ws"), dict(norm_weight=1.0)):
+        with pytest.raises(TypeError, match="torch tensor"):
+            csa.kv_append_fp4(**{**good, **a})
+    with pytest.raises(ValueError, match="ws must be a CUDA tensor"):
+        csa.kv_append_fp4(**good)
+    with pytest.raises(ValueError, match=r"idx_key must be torch.bfloat16 of shape \[3, 128\]"):
+        csa.kv_append_fp4(**{**good, "idx_key": bf(128, 3)})
+    with pytest.raises(ValueError):
+        csa.kv_unpack_fp4(layer, batch, cu, torch.tensor(0.0).bfloat16(), ws)
+    batch.B = 2 ** 40
+    with pytest.raises(OverflowError):
+        csa.kv_append_fp4(**good)
+    del batch.B
+    with pytest.raises(AttributeError):
+        csa.kv_append_fp4(**good)
+    for f, n in ((mod.kv_append_fp4, 8), (mod.kv_unpack_fp4, 7), (mod.bind, 1)):
+        with pytest.raises(TypeError):
+            f(*[None] * n)
+    with pytest.raises(ValueError):
+        mod.bind(0, 0)
