@@ -6,27 +6,30 @@
 //
 // Append: one warp per token, with the arithmetic of pack.cu (pack_token.cuh); the token's sequence, page,
 // rotation and window slot are worked out from its row number, so the caller builds no slot or angle
-// arrays and no pass over the latents comes before the pack.  Unpack: the inverse for the FP4 entries, e2m1 * e4m3 in bf16, which is exact
-// (at most 6 significant bits); a lane converts two pieces of 8 channels so that a warp's stores are
-// 512 contiguous bytes.  Both stream their bytes once.  Long unpacks are bound by HBM (200,003 entries:
-// 44 us, 5.9 TB/s), long appends by the instructions of norm, rotation and pack (65,536 tokens: 42 us, 3.0 TB/s, about
-// 460 warp instructions a token), short calls by the chain of dependent metadata loads (cu_rows, then the page id, then
-// the entry), which the tokens of an unpacking warp share.  Both are dependent launches, in place when
-// the kernel before them ends (8 tokens appended and read back: 10.2 -> 7.8 us).
+// arrays and no pass over the latents comes before the pack.  Unpack: the inverse for the FP4 entries,
+// e2m1 * e4m3 in bf16, which is exact (at most 6 significant bits); a lane converts two pieces of 8
+// channels so that a warp's stores are 512 contiguous bytes.
+//
+// Both stream their bytes once.  Long unpacks are bound by HBM (200,003 entries: 43 us, 6.0 TB/s), long appends
+// by the instructions of norm, rotation and pack (65,536 tokens: 39 us, 3.3 TB/s, about 460 warp
+// instructions a token), short calls by the chain of dependent metadata loads (cu_rows, then the page id, then
+// the entry), which the tokens of an unpacking warp share.  Both are dependent launches, in place when the
+// kernel before them ends (8 tokens appended and read back: 10.2 -> 7.8 us).
 #include "pack_token.cuh"
 #include "pipeline.cuh"
 #include "runs.cuh"
 
 namespace csa {
 
-constexpr int kRunWarps = 8;             // warps per CTA
-constexpr int kUnpackTok = 4;            // tokens per unpacking warp: 46 us for 200,003 entries (1: 54)
+constexpr int kRunWarps = 4;             // warps per CTA: a CTA's place is free again when its slowest token is done (8: 58.2 us for
+                                         // 65,536 tokens appended and read back, 4: 56.3, 2: 54.8 but 17.7 instead of 14.9 for 20,001)
+constexpr int kUnpackTok = 4;            // tokens per unpacking warp (in CTAs of 8 warps, 200,003 entries: 46 us; 1: 54)
 constexpr int kRunLargeFrom = 4096;      // rows from which unpacking warps take several tokens
 
 // 40 warps on an SM hide a token's chain of conversions and shuffles better than several tokens per warp do: 65,536
-// tokens 42 us (2 tokens per warp, 32 warps: 45; 4 tokens in 98 registers: 66).
+// tokens 42 us in CTAs of 8 warps (2 tokens per warp, 32 warps: 45; 4 tokens in 98 registers: 66).
 template <bool kNorm, bool kRope>
-__global__ void __launch_bounds__(32 * kRunWarps, 5) kv_append_kernel(csa_kv_layer layer, Runs r,
+__global__ void __launch_bounds__(32 * kRunWarps, 10) kv_append_kernel(csa_kv_layer layer, Runs r,
                                                                    const uint16_t *__restrict__ latent,
                                                                    const uint16_t *__restrict__ idx_key,
                                                                    const float *__restrict__ norm_w,
@@ -49,6 +52,9 @@ __global__ void __launch_bounds__(32 * kRunWarps, 5) kv_append_kernel(csa_kv_lay
     const bool no_rotation = kRope && p[0].pos >= rope_positions;
     if ((p[0].bad || no_rotation) && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
     if (p[0].seq < 0 || no_rotation) return;
+    const float *rope_row = kRope ? rope_table + (size_t)p[0].pos * kRopeRow : nullptr;
+    // the rotation is needed behind the norm: on its way meanwhile (65,536 tokens: 1 us less)
+    if (kRope && lane >= 28) asm volatile("prefetch.global.L2 [%0];" ::"l"(rope_row + 16 * (lane - 28)));
     in.s = p[0].slot;
     in.ss = -1;
     if (layer.swa && p[0].pos >= p[0].len - kWindow) {
@@ -56,7 +62,7 @@ __global__ void __launch_bounds__(32 * kRunWarps, 5) kv_append_kernel(csa_kv_lay
         if (row >= 0 && row < layer.num_rows) in.ss = row * kWindow + p[0].pos % kWindow;
         else if (row != -1 && lane == 0) report(ws, CSA_ERR_DEVICE_DATA, t);
     }
-    pack_token<kNorm, kRope>(layer, in, t, lane, ws, norm_w, kRope ? rope_table + (size_t)p[0].pos * kRopeRow : nullptr);
+    pack_token<kNorm, kRope>(layer, in, t, lane, ws, norm_w, rope_row);
 }
 
 template <int kTok>
