@@ -427,8 +427,8 @@ def _runs():
         try:
             from . import _runs as mod
         except ImportError as e:
-            raise RuntimeError("_runs.so is missing or does not load: build it with "
-                               "python -m fp4_compressed_sparse_kv_b200.build") from e
+            raise ImportError("_runs.so is missing or does not load; build it with "
+                              "`python -m fp4_compressed_sparse_kv_b200.build`") from e
         mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.csa_kv_append_fp4, L.csa_kv_unpack_fp4)))
         _runs_mod = mod
     return _runs_mod
