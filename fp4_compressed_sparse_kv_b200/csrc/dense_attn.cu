@@ -920,14 +920,18 @@ __device__ __noinline__ uint32_t dense_scores(int pi, uint32_t g0, uint32_t n_se
                 else
                     a.part_ml[(size_t)(2 * (blockIdx.x >> 1) + (pc.first ? 1 : 0)) * kDenseRows + hl] = make_float2(M - kPOffset, l);
             }
-            if (ok) {
+            // Only quarters with rows send: the scores that came from the other CTA in this piece show that it has
+            // stored the last piece's rows and read their inv.  A quarter without rows has waited for nothing of this
+            // piece from there, and its inv is of no use.
+            if (ok && active) {
                 ms.inv[hl] = inv;
                 st_async4(remote_addr(smem_addr(&ms.inv[hl]), peer), __float_as_uint(inv),
                           remote_addr(smem_addr(&ms.inv_full), peer));
             }
         }
         __syncwarp();
-        lane0_arrive_expect_tx(&ms.inv_full, 64u, lane);
+        if (active) lane0_arrive_expect_tx(&ms.inv_full, 64u, lane);
+        else lane0_arrive(&ms.inv_full, lane);
     }
     return ok ? sent : kDnFailed;
 }
