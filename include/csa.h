@@ -415,7 +415,7 @@ csa_status csa_kv_unpack_fp4(const csa_kv_layer *layer, const csa_batch *batch, 
  * csa_dense_attn -- attention of a run's query rows over every visible position of the FP4 cache (no
  * selection, no window ring): for head h of row t at position p, over the positions j it sees,
  *     s_j = sm_scale * q_h . v_j
- *     s_j = softcap * tanh(s_j / softcap)      if softcap > 0 (1e-20 .. 1e30)
+ *     s_j = softcap * tanh(s_j / softcap)      if softcap > 0 (1e-20 .. 1e30; within 2^-19 of itself)
  *     s_j = s_j - slopes[h] * |p - j|          if slopes
  *     out_h = sum_j e^{s_j} v_j / sum_j e^{s_j},  lse_h = log sum_j e^{s_j}
  *   q        bf16 [rows][H][512], 1 <= H <= 128
