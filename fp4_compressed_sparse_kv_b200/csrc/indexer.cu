@@ -248,10 +248,11 @@ __global__ void __launch_bounds__(kTopkThreads, 1) topk_kernel(const float *__re
     __shared__ uint32_t wcount[2][kTopkWarps];
     __shared__ uint32_t sel[2];
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    // the next kernel (the attention) may start its own preparation while the selection runs; the
-    // scores are read only once the previous grid (the block scorer) has finished
-    grid_dep_launch();
+    // the scores are read only once the previous grid (the block scorer) has finished; then the next kernel (the
+    // attention) may start its own preparation, which reads what kernels before the previous one wrote (its q),
+    // while the selection runs
     grid_dep_wait();
+    grid_dep_launch();
     const int L = seq_len[b];
     int n;
     if (L < 1 || L > max_seq_len) {
@@ -324,10 +325,10 @@ __global__ void reuse_kernel(const int32_t *__restrict__ prev, const int32_t *__
                              int32_t *__restrict__ out, int32_t *__restrict__ out_count, int out_cap, void *ws)
 {
     const int b = blockIdx.x;
-    // the next kernel (the layer's attention) may start its own preparation while this copy runs;
-    // the previous layer's set is read only once the previous grid has finished
-    grid_dep_launch();
+    // the previous layer's set is read only once the previous grid has finished; then the next kernel (the layer's
+    // attention) may start its own preparation, which reads its q, while this copy runs
     grid_dep_wait();
+    grid_dep_launch();
     int n = prev_count[b];
     if (n < 0 || n > prev_cap || n > out_cap) {
         if (threadIdx.x == 0) report(ws, CSA_ERR_DEVICE_DATA, b);

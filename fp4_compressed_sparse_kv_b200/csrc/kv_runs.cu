@@ -36,8 +36,8 @@ __global__ void __launch_bounds__(32 * kRunWarps, 10) kv_append_kernel(csa_kv_la
                                                                    const float *__restrict__ rope_table,
                                                                    int rope_positions, void *ws)
 {
-    grid_dep_launch();   // a dependent kernel waits for this grid before it reads the caches
-    grid_dep_wait();     // and this one for the kernel before it: what follows reads and overwrites its data
+    grid_dep_wait();     // what follows reads and overwrites the data of the kernel before it
+    grid_dep_launch();   // only now: a dependent kernel may read at its start what any kernel before this one wrote
     const int t = blockIdx.x * kRunWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (t == 0 && lane == 0 && r.cu_rows[r.B] > r.rows) report(ws, CSA_ERR_DEVICE_DATA, r.B);
@@ -69,8 +69,8 @@ template <int kTok>
 __global__ void __launch_bounds__(32 * kRunWarps) kv_unpack_kernel(csa_kv_layer layer, Runs r,
                                                                    uint16_t *__restrict__ latent, void *ws)
 {
-    grid_dep_launch();
     grid_dep_wait();
+    grid_dep_launch();
     const int t0 = (blockIdx.x * kRunWarps + (threadIdx.x >> 5)) * kTok;
     const int lane = threadIdx.x & 31;
     if (t0 == 0 && lane == 0 && r.cu_rows[r.B] > r.rows) report(ws, CSA_ERR_DEVICE_DATA, r.B);

@@ -112,7 +112,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // Programmatic dependent launch.  grid_dep_wait: wait until the previous grid of the stream has
 // completed and its memory is visible (call before touching anything it writes); grid_dep_launch:
 // allow the next grid of the stream to be scheduled.  Both do nothing for grids launched without the
-// programmatic-serialization attribute.
+// programmatic-serialization attribute.  A kernel that is itself a dependent launch waits before it allows the next one,
+// unless that one can only be its own combine: what the next kernel does before its own wait (the attention reads q) has
+// to come after every kernel before this one, and the wait is what says that they are complete.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
