@@ -19,12 +19,16 @@ struct PackIn {
     int32_t ss;     // window slot
 };
 
-// x / c where only its place among borders of few bits counts (inv: 1 / c, rounded): the product, within 2^-22 of the
-// quotient, rounded to 11 significant bits.  A quotient that is a number t of at most 11 bits gives t; one that is 2^-8 of
-// itself away from t stays on its side of it.  Zeros keep their sign, infinities and NaN pass.
+// x / c where only its place among borders of few bits counts.  inv: 1 / c rounded, times 1 + 2^-20, so that the product is
+// above the quotient, by less than 2^-19 of it; its first 11 significant bits are then those of a quotient that is a
+// number t of at most 11 bits, and a quotient that is 2^-8 of itself away from t stays on its side of it.  Zeros keep their
+// sign; infinities pass, and a NaN stays one (the product's NaN is 0x7FFFFFFF: rounding it by an addition would carry
+// into the sign and leave a zero).
+constexpr float kNearAbove = 1.f + 0x1p-20f;
+
 __device__ __forceinline__ float near_quotient(float x, float inv)
 {
-    return __uint_as_float((__float_as_uint(__fmul_rn(x, inv)) + 0x1000u) & 0xFFFFE000u);
+    return __uint_as_float(__float_as_uint(__fmul_rn(x, inv)) & 0xFFFFE000u);
 }
 
 // Pack token `tok` (its number in a report of a bad slot).  kNorm: RMSNorm with weights norm_w first;
@@ -93,11 +97,11 @@ __device__ __forceinline__ void pack_token(const csa_kv_layer &layer, const Pack
         // (E4M3) and 3 (E2M1) significant bits, so t * 6 and t * s have at most 7, x has 8 (it is a bf16 value),
         // and a quotient that is not exactly t is at least 2^-8 of it away.  (Seventeen divisions less per lane:
         // 65,536 tokens appended with norm and rotation: 80 -> 66 us.)
-        const uint8_t sc = (uint8_t)(f32x2_to_e4m3x2(near_quotient(amax, 1.0f / 6.0f), 0.f) & 0xFF);
+        const uint8_t sc = (uint8_t)(f32x2_to_e4m3x2(near_quotient(amax, kNearAbove / 6.0f), 0.f) & 0xFF);
         const float sd = e4m3_to_f32(sc);
         uint2 codes = make_uint2(0u, 0u);
         if (sd != 0.f) {
-            const float inv = __frcp_rn(sd);
+            const float inv = __fmul_rn(__frcp_rn(sd), kNearAbove);
             float y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) y[i] = near_quotient(x[i], inv);
