@@ -9,6 +9,7 @@ Python binding against PyTorch's headers, becomes _runs.so.
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -21,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libcsa.so")
 RUNS = os.path.join(HERE, "_runs.so")
+RUNS_STAMP = os.path.join(BUILD, "_runs.stamp")   # what _runs.so was built against
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -53,12 +55,17 @@ def _compile(src, verbose_ptxas):
 def _build_binding():
     src = os.path.join(CSRC, "run_binding.cpp")
     deps = [src, os.path.join(INCLUDE, "csa.h")]
-    if os.path.exists(RUNS) and os.path.getmtime(RUNS) >= max(os.path.getmtime(d) for d in deps):
+    # PyTorch's C++ interface and Python's differ from version to version
+    version = importlib.metadata.version("torch")
+    stamp = "torch %s\npython %s\n" % (version, sys.version)
+    if os.path.exists(RUNS) and os.path.getmtime(RUNS) >= max(os.path.getmtime(d) for d in deps) \
+            and os.path.exists(RUNS_STAMP) and open(RUNS_STAMP).read() == stamp:
         return
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = RUNS + ".tmp.%d" % os.getpid()
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Werror", "-I", INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Werror", "-I", INCLUDE,
+           '-DCSA_TORCH_VERSION="%s"' % version]
     for inc in (os.path.join(torch, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
         cmd += ["-isystem", inc]
     cmd += [src, "-o", tmp, "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -66,6 +73,8 @@ def _build_binding():
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
     os.replace(tmp, RUNS)
+    with open(RUNS_STAMP, "w") as f:
+        f.write(stamp)
 
 
 def build(verbose_ptxas: bool = False, quiet: bool = True) -> str:

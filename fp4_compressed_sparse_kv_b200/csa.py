@@ -429,6 +429,10 @@ def _runs():
         except ImportError as e:
             raise ImportError("_runs.so is missing or does not load; build it with "
                               "`python -m fp4_compressed_sparse_kv_b200.build`") from e
+        built_for = getattr(mod, "torch_version", "another version")
+        if built_for != torch.__version__:
+            raise ImportError("_runs.so was built for PyTorch %s and this is %s; build it again with "
+                              "`python -m fp4_compressed_sparse_kv_b200.build`" % (built_for, torch.__version__))
         mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.csa_kv_append_fp4, L.csa_kv_unpack_fp4)))
         _runs_mod = mod
     return _runs_mod

@@ -258,5 +258,11 @@ PyMODINIT_FUNC PyInit__runs(void)
         if (!(names[i] = PyUnicode_InternFromString(kNames[i]))) return nullptr;
     if (!(max_seq_len_name = PyUnicode_InternFromString("max_seq_len"))) return nullptr;
     if (!(cuda_stream_name = PyUnicode_InternFromString("cuda_stream"))) return nullptr;
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    // the PyTorch whose headers this was compiled with (build.py names it): csa.py refuses it under another one
+    if (m && PyModule_AddStringConstant(m, "torch_version", CSA_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }
