@@ -510,7 +510,7 @@ def dense_attn(layer, batch, cu_rows, q, out, lse, ws, sm_scale=None, softcap=0.
     """Attention of a ragged run's queries q (bf16 [rows, H, 512], H <= 128) over every visible position of
     the FP4 cache: out bf16 [rows, H, 512], lse float32 [rows, H].  Causal, or spans int32 [rows, 2] of the
     positions lo <= j < hi each row sees; softcap > 0 caps scores by softcap * tanh(s / softcap); slopes
-    float32 [H] subtracts slopes[h] * |p - j|."""
+    float32 [H] subtracts slopes[h] * |p - j|.  The window ring, which sparse_decode_attn adds, takes no part."""
     rows, H = q.shape[0], q.shape[1]
     _run_rows(batch, cu_rows)
     _run_array(q, "q", torch.bfloat16, (rows, H, LATENT))

@@ -33,9 +33,9 @@
 // half of the softmax's chain (read S, send, receive, maximum, exp2, P to both CTAs, PV, P buffer free: 4,600 cycles):
 // two groups of warps take the tiles in turn, and a third does not fit the two S and P buffers that TMEM and shared
 // memory leave.  A row tile costs 16,000 cycles more (Q into TMEM, the last tiles' chain, O out), and a call 15 us before
-// and after (plan, first pages, partials, combine).  Measured: 2,048 rows of 64 heads behind 14,336 positions 4.2-4.4 ms
-// (1.0 PFLOP/s, at the power limit); one row of each of 8 sequences of 131,072 positions, 64 heads (half of the tensor
-// rows idle): 270 us; one row of 16 heads over 4,096 positions: 23 us.
+// and after (plan, first pages, partials, combine).  Measured: 2,048 rows of 64 heads behind 14,336 positions 4.3-4.5 ms
+// (0.92-0.95 PFLOP/s, at the power limit); one row of each of 8 sequences of 131,072 positions, 64 heads (half of the tensor
+// rows idle): 270-279 us; one row of 16 heads over 4,096 positions: 23 us.
 #include <cuda_bf16.h>
 
 #include "attention_tile.cuh"
@@ -74,7 +74,9 @@ constexpr uint32_t kDnTmemCols = 512;
 constexpr uint32_t kDnColO = 0;                  // O_x: 256 channels
 constexpr uint32_t kDnColQ = 256;                // Q_x: 256 channels, two per column
 constexpr uint32_t kDnColS = 384;                // S_x of tile g: columns 384 + 64(g%2) ..
-constexpr long long kDnMinTiles = 4;             // pages a cluster takes at least (one row tile of 64 pages: 27.5 us; 2: 30.7)
+constexpr long long kDnMinTiles = 4;             // a cluster's least share of the line, in pages (a row tile's fixed kDnPieceCost
+                                                 // counted, so a share inside that has no page: of a tile of 64 pages, 18
+                                                 // shares, 16 clusters take pages).  That tile: 23.2 us; 2: 24.6; 8: 25.6
 constexpr int kDnPieceCost = 8;                  // what a row tile costs besides its pages, in pages
 constexpr float kDnNoMax = -3.402823466e38f;     // reference of a row that has seen nothing: no finite score is below it
 static_assert(kTile == kPage, "a tile is one page");
@@ -641,9 +643,9 @@ __device__ __noinline__ uint32_t dense_mma(int pi, uint32_t g0, uint32_t n_go)
 }
 
 // The order of a piece's pages: with a distance bias from the last to the first, so that the newest positions set the
-// rows' references and O is hardly ever rescaled (23 rows of six sequences of 50,021 positions: 149 us, upwards 204);
-// otherwise upwards, so that the page that causal rows see in part comes last (2,048 rows behind 14,336 positions:
-// 4,514 us, downwards 4,595).
+// rows' references and O is hardly ever rescaled (23 rows of six sequences of 50,021 positions: 129 us, upwards 167);
+// otherwise upwards, so that the page that causal rows see in part comes last (no difference beyond the noise: 2,048
+// rows behind 14,336 positions 4.44-4.52 ms, downwards 4.53).
 struct PageOrder {
     int first, step;
     __device__ __forceinline__ PageOrder(const DenseArgs &a, const DensePiece &pc)

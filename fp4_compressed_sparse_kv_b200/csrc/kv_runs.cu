@@ -10,19 +10,21 @@
 // e2m1 * e4m3 in bf16, which is exact (at most 6 significant bits); a lane converts two pieces of 8
 // channels so that a warp's stores are 512 contiguous bytes.
 //
-// Both stream their bytes once.  Long unpacks are bound by HBM (200,003 entries: 43 us, 6.0 TB/s), long appends
-// by the instructions of norm, rotation and pack (65,536 tokens: 39 us, 3.3 TB/s, about 460 warp
-// instructions a token), short calls by the chain of dependent metadata loads (cu_rows, then the page id, then
-// the entry), which the tokens of an unpacking warp share.  Both are dependent launches, in place when the
-// kernel before them ends (8 tokens appended and read back: 10.2 -> 7.8 us).
+// Both stream their bytes once.  Long unpacks are bound by HBM (200,003 entries: 44 us, 5.9 TB/s).  Long appends are
+// bound by instructions and the latency of the metadata's loads together: 65,536 tokens with norm and rotation 40 us
+// (3.3 TB/s, 449 warp instructions a token issued in 68 % of the cycles), 20,001 ready tokens 10.2 us (265 a token in
+// 59 %, the commonest stall a global load; its 5,001 CTAs are 3.4 rounds of the SMs).  Short calls are bound by the metadata's loads, one behind
+// the other (cu_rows, then the page id, then the entry), which the tokens of an unpacking warp share.  Both are dependent launches,
+// in place when the kernel before them ends (8 tokens appended and read back: 10.2 -> 7.5-8.2 us).
 #include "pack_token.cuh"
 #include "pipeline.cuh"
 #include "runs.cuh"
 
 namespace csa {
 
-constexpr int kRunWarps = 4;             // warps per CTA: a CTA's place is free again when its slowest token is done (8: 58.2 us for
-                                         // 65,536 tokens appended and read back, 4: 56.3, 2: 54.8 but 17.7 instead of 14.9 for 20,001)
+constexpr int kRunWarps = 4;             // warps per CTA: a CTA's place is free again when its slowest token is done (65,536 normed
+                                         // and 20,001 ready tokens appended and read back: 8 warps 57.1 and 17.6 us, 4: 55.3
+                                         // and 17.2, 2: 54.9 and 18.1)
 constexpr int kUnpackTok = 4;            // tokens per unpacking warp (in CTAs of 8 warps, 200,003 entries: 46 us; 1: 54)
 constexpr int kRunLargeFrom = 4096;      // rows from which unpacking warps take several tokens
 

@@ -10,7 +10,7 @@
 // Lane g owns 16-channel group g of the 512-channel latent, which is exactly one E4M3 scale: its amax
 // needs no cross-lane step, and its 16 codes are one 8-byte store.  The window entry needs the
 // token's amax, a 5-step warp max.  Loads are 2 x 16 B per lane (latent) and 8 B per lane (key), all
-// coalesced; long calls are HBM-bound streaming (65,536 tokens, 112 MB: 24.8 us, 4.5 TB/s; 43 us with a
+// coalesced; long calls are HBM-bound streaming (65,536 tokens, 112 MB: 25.0 us, 4.5 TB/s; 43 us with a
 // division per value).
 //
 // The norm variant starts from the pre-norm latent (ailily.cc article, section 三: the KV latent is

@@ -428,6 +428,9 @@ csa_status csa_kv_unpack_fp4(const csa_kv_layer *layer, const csa_batch *batch, 
  * accumulation and sums, probabilities rounded to fp16 once, out rounded to bf16 once.  Rows of non-finite q, and rows that see an
  * entry with a NaN scale, give NaN; no other row does.  Results do not depend on timing, but rounding
  * depends on how the call's rows divide over the GPU.  Every position of a bad page is left out.
+ * The FP8 window takes no part: csa_sparse_decode_attn adds it to its softmax as a second segment, so a drafted token
+ * attended here and the same token decoded there with a window get different outputs.  The two agree (to their
+ * roundings) with swa_row = -1 and every block selected.
  * ws: csa_dense_attn_workspace_bytes() bytes, whatever the sizes.
  */
 size_t csa_dense_attn_workspace_bytes(void);
